@@ -28,6 +28,14 @@
  *                        (mobi_pack_slices: one width per slice); the GEMM
  *                        entry points' _bits / _slices forms read them.
  *   mobi_ckpt_*          many-in-one checkpoints of packed layers.
+ * and, beside the mixed-bit layer, what a model around it runs:
+ *   mobi_fp8_quant       activations or weights to e4m3 with a scale per block of 128.
+ *   mobi_fp8_gemm        the 8-bit layer: y = x W^T on such operands.
+ *   mobi_fp8_gated       act(x Wg^T) * (x Wu^T) on such operands.
+ *   mobi_norm            norm after a block, gate, residual scale and the next
+ *                        block's norm in one pass.
+ *   mobi_logprobs        log probabilities of given tokens, entropy and top
+ *                        alternatives from logits.
  *   mobi_gemm_path, mobi_gemm_decode_noalloc, mobi_sync_check and the size
  *   and status helpers.
  *
@@ -558,6 +566,136 @@ MOBI_API mobi_status mobi_sync_check(void* stream);
  * Test use only.
  */
 MOBI_API mobi_status mobi_debug_set_wait_limit(int64_t limit);
+
+/* ---- the 8-bit layer, the norm between blocks, the scoring of logits --------------
+ *
+ * Element types of these calls. MOBI_E4M3 is the 8-bit float with 4 exponent
+ * and 3 mantissa bits, no infinities, largest value 448.
+ */
+enum { MOBI_F32 = 0, MOBI_BF16 = 1, MOBI_F16 = 2, MOBI_E4M3 = 3 };
+
+/*
+ * Blocks of 128 values as e4m3 with one fp32 scale each.
+ *
+ * A block is 1 x 128 (block_rows = 1: activations, one token's values of one
+ * group of 128 along K) or 128 x 128 (block_rows = 128: weights). With
+ * a = max |x| over the block,
+ *   s = max(a / 448, 2^-126)          (fp32)
+ *   q = e4m3(x * (1 / s))             (both in fp32; to nearest even, saturating)
+ * so q * s stands for x. A block that holds a NaN or an infinity gets a NaN or
+ * infinite scale and NaN codes in its place: whatever it enters becomes NaN.
+ *
+ *   X      [T][K] of `dtype` (MOBI_F32, MOBI_BF16 or MOBI_F16), row pitch ldx
+ *          elements (>= K); aligned to its element.
+ *   Q      [T][K] e4m3 bytes, row pitch ldq bytes (>= K). The products below
+ *          take ldq % 16 == 0 and a 16-byte aligned Q; columns K .. ldq are
+ *          left as they were.
+ *   scale  fp32 [ceil(K/128)][ceil(T/block_rows)], group-major like sz.
+ * T = 0 or K = 0: nothing is written. T <= 2^28; K <= 2^23 (block_rows = 1) or 2^28, and at
+ * most 2^31 - 1 blocks of weights.
+ */
+MOBI_API mobi_status mobi_fp8_quant(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, int block_rows,
+                                    void* Q, int64_t ldq, float* scale, void* stream);
+
+/*
+ * The 8-bit layer:
+ *   Y[t][n] = sum_b xs[b][t] * wsc[b][n / 128] * sum_{k in block b} X[t][k] W[n][k]
+ * with exact products, fp32 sums and one rounding to out_dtype at the end.
+ *
+ *   X, xs    e4m3 [T][K] with row pitch ldx bytes, fp32 [ceil(K/128)][T] (block_rows = 1).
+ *   W, wsc   e4m3 [N][K] with row pitch ldw bytes, fp32 [ceil(K/128)][ceil(N/128)] (block_rows = 128).
+ *   Y        [T][N] of out_dtype (MOBI_F32, MOBI_BF16 or MOBI_F16), row pitch ldy elements
+ *            (>= N); aligned to its element (16-byte aligned rows are written faster).
+ * X and W are 16-byte aligned with pitches that are multiples of 16
+ * (MOBI_ERR_MISALIGNED otherwise); any K >= 1, N and T, up to 2^28 each. A ragged last
+ * block of K is allowed. No workspace. The result depends on the sizes' work
+ * split (sums of K ranges are added in a fixed order), not on timing.
+ */
+MOBI_API mobi_status mobi_fp8_gemm(const void* X, int64_t ldx, const float* xs, int64_t T, int64_t K, const void* W,
+                                   int64_t ldw, const float* wsc, int64_t N, int out_dtype, void* Y, int64_t ldy,
+                                   void* stream);
+
+/* Activations of mobi_fp8_gated: g / (1 + e^-g); g Phi(g); its tanh form; max(g, 0). */
+enum { MOBI_ACT_SILU = 0, MOBI_ACT_GELU = 1, MOBI_ACT_GELU_TANH = 2, MOBI_ACT_RELU = 3 };
+
+/*
+ * The gated product of a feed-forward block in one kernel:
+ *   H[t][n] = act(g[t][n]) * u[t][n],  g = X Wg^T, u = X Wu^T as in mobi_fp8_gemm.
+ * Neither g nor u is written. With out_dtype MOBI_E4M3, H is requantised in
+ * blocks of 128 columns as mobi_fp8_quant does (block_rows = 1), ready for the next
+ * product: hs is fp32 [ceil(N/128)][T] and ldh is in bytes; otherwise hs is
+ * not used and may be NULL. Operands and errors as in mobi_fp8_gemm.
+ */
+MOBI_API mobi_status mobi_fp8_gated(const void* X, int64_t ldx, const float* xs, int64_t T, int64_t K, const void* Wg,
+                                    int64_t ldg, const float* gs, const void* Wu, int64_t ldu, const float* us,
+                                    int64_t N, int act, int out_dtype, void* H, int64_t ldh, float* hs, void* stream);
+
+/* Kinds of norm: v itself; v / sqrt(mean(v^2) + eps); (v - mean(v)) / sqrt(var(v) + eps). */
+enum { MOBI_NORM_NONE = 0, MOBI_NORM_RMS = 1, MOBI_NORM_LAYER = 2 };
+
+/*
+ * The step between two blocks of a model, one pass over its rows:
+ *   z = post(block) * post_weight + post_bias          (post: NONE leaves z = block)
+ *   r = x + scale * gate * z
+ *   n = norm(r) * weight + bias
+ * in fp32 from the inputs to one rounding at each output; the norm takes r
+ * before its rounding. Without a block (block = NULL) r = x: a plain norm, and
+ * post, gate, scale and r_out are not used.
+ */
+typedef struct mobi_norm_args {
+  const void* x;            /* [T][D] residual stream, x_dtype, row pitch ldx */
+  const void* block;        /* [T][D] the block's output, block_dtype, row pitch ldb; or NULL */
+  const void* gate;         /* gate_dtype; element (t, d) at t * gate_st + d * gate_sd (0 strides broadcast); or NULL */
+  const void* weight;       /* [D] weight_dtype; or NULL (1) */
+  const void* bias;         /* [D] weight_dtype; or NULL (0) */
+  const void* post_weight;  /* [D] weight_dtype; or NULL (1) */
+  const void* post_bias;    /* [D] weight_dtype; or NULL (0) */
+  void* r_out;              /* [T][D] x_dtype, row pitch ldr: r; may be x itself; or NULL */
+  void* n_out;              /* [T][D] out_dtype, row pitch ldn: n */
+  float* n_scale;           /* out_dtype MOBI_E4M3: fp32 [ceil(D/128)][T], as mobi_fp8_quant (block_rows = 1) */
+  int64_t T, D, ldx, ldb, ldr, ldn, gate_st, gate_sd;
+  int x_dtype, block_dtype, gate_dtype, weight_dtype, out_dtype;
+  int post, kind;           /* MOBI_NORM_* */
+  float eps, post_eps, scale;
+  int unit_offset;          /* nonzero: weights count as 1 + weight */
+} mobi_norm_args;
+
+/*
+ * x, block, gate and the weights are MOBI_F32, MOBI_BF16 or MOBI_F16; n also
+ * MOBI_E4M3. Every pointer is aligned to its element (16-byte aligned rows are read and
+ * written faster). T = 0: nothing. D from 1 to 16384 (MOBI_ERR_UNSUPPORTED_SHAPE beyond),
+ * T <= 2^28; pitches >= D; eps, post_eps >= 0 and scale finite. Outputs do not overlap the inputs or each
+ * other, except r_out = x with the same pitch.
+ */
+MOBI_API mobi_status mobi_norm(const mobi_norm_args* args, void* stream);
+
+/*
+ * Scoring of logits: with d = (logits - max) / temperature over a row,
+ * S = sum e^d and p = e^d / S,
+ *   logprob[t]  = d[target] - ln S
+ *   entropy[t]  = -sum p ln p = ln S - (sum e^d d) / S
+ *   top_logprob, top_index [t][0 .. top_k): the largest logits in descending
+ *                 order, the lowest index first among equal ones, and their
+ *                 log probabilities.
+ *
+ *   logits   [T][V] of `dtype` (MOBI_F32, MOBI_BF16 or MOBI_F16), row pitch ld elements (>= V);
+ *            aligned to its element. -infinity shuts an entry out: its log
+ *            probability is -infinity and it is never an alternative.
+ *   targets  int64 [T], or NULL (logprob is then not written). A negative
+ *            target is ignored: logprob 0. A target >= V gives NaN and is
+ *            reported by mobi_sync_check as MOBI_ERR_INVALID_ARG.
+ *   logprob, entropy  fp32 [T]; entropy may be NULL.
+ *   top_logprob, top_index  fp32 and int32 [T][top_k], contiguous; 0 <= top_k <= 32.
+ *            Where fewer than top_k entries are above -infinity, the rest is
+ *            -infinity with index -1.
+ * A row with nothing above -infinity gives logprob -infinity and entropy 0. A
+ * row with a NaN or +infinity gives NaN log probabilities and entropy; its
+ * alternatives are then unspecified indices of the row (or -1).
+ * T = 0: nothing. T, V <= 2^28, V >= 1; temperature finite and at least 1e-30.
+ */
+MOBI_API mobi_status mobi_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                   const int64_t* targets, float temperature, int top_k, float* logprob,
+                                   float* entropy, float* top_logprob, int32_t* top_index, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,12 @@ Entry points (same names as the C ABI; `bits=` selects the *_bits form and
   mobi_gemm_grouped(problems)       the GEMM half of it (k_t given)
   mobi_ckpt_save / MobiCheckpoint   many-in-one checkpoint of packed layers (load any slice count)
   mobi_sync_check()                 sync + device-side error word
+and, around the mixed-bit layer (blocks.py):
+  mobi_fp8_quant(X, block_rows)     blocks of 128 as e4m3 with a scale each -> (codes, scales)
+  mobi_fp8_gemm(X, xs, W, ws)       the 8-bit layer y = x W^T
+  mobi_fp8_gated(X, xs, Wg, gs, Wu, us, act)  act(x Wg^T) * (x Wu^T) in one kernel
+  mobi_norm(x, weight, block=...)   norm after a block, gate, residual scale, next norm -> (n, r)
+  mobi_logprobs(logits, targets, temperature, top_k)  log probabilities, entropy, top alternatives
 """
 from __future__ import annotations
 
@@ -27,6 +33,9 @@ import os
 
 import torch
 
+from . import blocks as _blocks
+from .blocks import mobi_fp8_gated, mobi_fp8_gemm, mobi_fp8_quant, mobi_logprobs, mobi_norm
+
 __all__ = [
     "MobiError", "lib", "mobi_version", "mobi_status_string", "mobi_codes_bytes", "mobi_sz_bytes",
     "mobi_route_workspace_bytes", "mobi_gemm_workspace_bytes", "mobi_pack", "mobi_route", "mobi_gemm", "mobi_last_error",
@@ -34,6 +43,7 @@ __all__ = [
     "mobi_linear_workspace_bytes", "mobi_route_mlp", "mobi_route_mlp_workspace_bytes", "mobi_linear_grouped",
     "mobi_linear_grouped_workspace_bytes", "mobi_gemm_grouped", "mobi_gemm_grouped_workspace_bytes", "MAX_GROUP",
     "mobi_ckpt_save", "MobiCheckpoint", "mobi_crc32c",
+    "mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_norm", "mobi_logprobs",
     "PATH_AUTO",
     "PATH_DECODE",
     "PATH_PREFILL", "EXPORTED_SYMBOLS",
@@ -80,7 +90,7 @@ EXPORTED_SYMBOLS = (
     "mobi_gemm_bits", "mobi_gemm_grouped_bits", "mobi_linear_bits", "mobi_linear_grouped_bits",
     "mobi_codes_bytes_slices", "mobi_pack_slices", "mobi_gemm_slices", "mobi_linear_slices",
     "mobi_gemm_grouped_slices", "mobi_linear_grouped_slices",
-)
+) + _blocks.SYMBOLS
 
 
 class MobiError(RuntimeError):
@@ -190,6 +200,7 @@ def lib() -> ctypes.CDLL:
         L.mobi_sync_check.restype = ci
         L.mobi_debug_set_wait_limit.argtypes = [i64]
         L.mobi_debug_set_wait_limit.restype = ci
+        _blocks.bind(L)
         _lib = L
     return _lib
 

@@ -1,0 +1,294 @@
+"""What a model runs around the mixed-bit layer: the 8-bit layer with a scale per
+block of 128, the step between two blocks (norms, gate, residual) and the
+scoring of logits. Bindings of the calls of the same names in include/mobi.h.
+
+Unlike the mixed-bit calls these take row pitches, so a tensor may be a slice of
+a larger one as long as its last dimension is contiguous, and they run on the
+tensors' device, on that device's current stream (or `stream`). Tensors of one
+call live on one device. Outputs are allocated unless given.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+E4M3 = torch.float8_e4m3fn
+_DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, E4M3: 3}
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+_NORM = {"none": 0, None: 0, "rms": 1, "layer": 2}
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+
+
+class NormArgs(ctypes.Structure):
+    """mobi_norm_args (include/mobi.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "block", "gate", "weight", "bias", "post_weight", "post_bias",
+                                                "r_out", "n_out", "n_scale")]
+                + [(n, ctypes.c_int64) for n in ("T", "D", "ldx", "ldb", "ldr", "ldn", "gate_st", "gate_sd")]
+                + [(n, ctypes.c_int) for n in ("x_dtype", "block_dtype", "gate_dtype", "weight_dtype", "out_dtype",
+                                               "post", "kind")]
+                + [(n, ctypes.c_float) for n in ("eps", "post_eps", "scale")]
+                + [("unit_offset", ctypes.c_int)])
+
+
+def bind(L: ctypes.CDLL) -> None:
+    """Argument types of the calls of this module."""
+    p, i64, ci, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    L.mobi_fp8_quant.argtypes = [p, ci, i64, i64, i64, ci, p, i64, p, p]
+    L.mobi_fp8_gemm.argtypes = [p, i64, p, i64, i64, p, i64, p, i64, ci, p, i64, p]
+    L.mobi_fp8_gated.argtypes = [p, i64, p, i64, i64, p, i64, p, p, i64, p, i64, ci, ci, p, i64, p, p]
+    L.mobi_norm.argtypes = [p, p]
+    L.mobi_logprobs.argtypes = [p, ci, i64, i64, i64, p, f32, ci, p, p, p, p, p]
+    for n in ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_norm", "mobi_logprobs"):
+        getattr(L, n).restype = ci
+
+
+SYMBOLS = ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_norm", "mobi_logprobs")
+
+_calls: dict = {}
+
+
+def _call(name: str, device: int, stream, *args) -> None:
+    """Run library call `name` on `device`, its last argument the stream."""
+    fn = _calls.get(name)
+    if fn is None:
+        from . import lib
+        fn = _calls[name] = getattr(lib(), name)
+    if _get_device() != device:
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    if stream is None:
+        s = _raw_stream(device)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = fn(*args, s)
+    if status:
+        from . import _check
+        _check(name, status)
+
+
+def _matrix(t: torch.Tensor, what: str, device=None):
+    """(rows, columns, row pitch) of a CUDA matrix whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    _on(t, what, device)
+    (R, C), (ld, sd) = t.shape, t.stride()
+    if C > 1 and sd != 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    if R <= 1:
+        ld = max(C, 1) if ld < C else ld
+    elif ld < C:
+        raise ValueError(f"the rows of {what} overlap")
+    return R, C, ld
+
+
+def _on(t: torch.Tensor, what: str, device=None) -> None:
+    if not t.is_cuda:
+        raise ValueError("libmobi takes CUDA tensors only (no CPU path)")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what} is on another device")
+
+
+def _vector(t, n: int, what: str, device, dtype=None):
+    """The address of a contiguous vector of n elements (None: no vector)."""
+    if t is None:
+        return None
+    _on(t, what, device)
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous vector of {n} elements")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    return t.data_ptr()
+
+
+def _scales(s: torch.Tensor, kb: int, rb: int, what: str, device) -> int:
+    _on(s, what, device)
+    if s.dtype is not torch.float32 or s.shape != (kb, rb) or not s.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 tensor of shape ({kb}, {rb})")
+    return s.data_ptr()
+
+
+def _out(t, shape, dtype, what, device, dev):
+    """A given output checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _on(t, what, device)
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
+    return t
+
+
+def _codes(T: int, K: int, dev) -> torch.Tensor:
+    """A new e4m3 [T, K] whose rows start at multiples of 16 bytes."""
+    ld = (K + 15) & ~15
+    q = torch.empty((T, ld), dtype=E4M3, device=dev)
+    return q if ld == K else q[:, :K]
+
+
+def mobi_fp8_quant(X: torch.Tensor, block_rows: int = 1, Q: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None, stream=None):
+    """X [T, K] (fp32, bf16 or fp16) in blocks of 1 x 128 (activations) or 128 x 128 (block_rows=128, weights)
+    -> (Q e4m3 [T, K], scale fp32 [ceil(K/128), ceil(T/block_rows)]); Q * scale stands for X."""
+    T, K, ldx = _matrix(X, "X")
+    dt = _DT.get(X.dtype, 3)
+    if dt == 3:
+        raise ValueError("X must be fp32, bf16 or fp16")
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError("block_rows must be 1 or 128")
+    d, dev = X.get_device(), X.device
+    kb, rb = (K + 127) >> 7, T if block_rows == 1 else (T + 127) >> 7
+    Q = _codes(T, K, dev) if Q is None else _out(Q, (T, K), E4M3, "Q", d, dev)
+    if scale is None:
+        scale = torch.empty((kb, rb), dtype=torch.float32, device=dev)
+    sp = _scales(scale, kb, rb, "scale", d)
+    _call("mobi_fp8_quant", d, stream, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), _matrix(Q, "Q", d)[2],
+          sp)
+    return Q, scale
+
+
+def _operand(Q, scale, what, rows, K, device):
+    """(rows, pitch, codes address, scales address) of an e4m3 operand; rows per scale `rows`."""
+    if Q.dtype is not E4M3:
+        raise ValueError(f"{what} must be e4m3")
+    R, k, ld = _matrix(Q, what, device)
+    if K is not None and k != K:
+        raise ValueError(f"{what} has {k} columns, X has {K}")
+    if R <= 1:
+        ld = (ld + 15) & ~15  # one row: the pitch is never used
+    return R, ld, Q.data_ptr(), _scales(scale, (k + 127) >> 7, (R + rows - 1) // rows, f"the scales of {what}", device)
+
+
+def mobi_fp8_gemm(X: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, ws: torch.Tensor, out_dtype=torch.float32,
+                  Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The 8-bit layer Y = X W^T: X e4m3 [T, K] with xs (block_rows=1), W e4m3 [N, K] with ws (block_rows=128)
+    -> Y [T, N] in out_dtype (fp32, bf16 or fp16)."""
+    d = X.get_device()
+    K = X.shape[-1]
+    T, ldx, xp, xsp = _operand(X, xs, "X", 1, None, None)
+    N, ldw, wp, wsp = _operand(W, ws, "W", 128, K, d)
+    dt = _DT.get(out_dtype, 3)
+    if dt == 3:
+        raise ValueError("out_dtype must be fp32, bf16 or fp16")
+    Y = _out(Y, (T, N), out_dtype, "Y", d, X.device)
+    _call("mobi_fp8_gemm", d, stream, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), _matrix(Y, "Y", d)[2])
+    return Y
+
+
+def mobi_fp8_gated(X: torch.Tensor, xs: torch.Tensor, Wg: torch.Tensor, gs: torch.Tensor, Wu: torch.Tensor,
+                   us: torch.Tensor, act: str = "silu", out_dtype=torch.bfloat16, H: torch.Tensor | None = None,
+                   hs: torch.Tensor | None = None, stream=None):
+    """act(X Wg^T) * (X Wu^T) in one kernel, operands as mobi_fp8_gemm; act "silu", "gelu", "gelu_tanh" or "relu".
+    -> H [T, N] in out_dtype, or (H e4m3, hs fp32 [ceil(N/128), T]) for out_dtype torch.float8_e4m3fn."""
+    d, dev = X.get_device(), X.device
+    K = X.shape[-1]
+    T, ldx, xp, xsp = _operand(X, xs, "X", 1, None, None)
+    N, ldg, gp, gsp = _operand(Wg, gs, "Wg", 128, K, d)
+    Nu, ldu, up, usp = _operand(Wu, us, "Wu", 128, K, d)
+    if Nu != N:
+        raise ValueError("Wg and Wu must have as many rows")
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)}")
+    dt = _DT.get(out_dtype)
+    if dt is None:
+        raise ValueError("out_dtype must be fp32, bf16, fp16 or e4m3")
+    hsp = None
+    if dt == 3:
+        H = _codes(T, N, dev) if H is None else _out(H, (T, N), E4M3, "H", d, dev)
+        if hs is None:
+            hs = torch.empty(((N + 127) >> 7, T), dtype=torch.float32, device=dev)
+        hsp = _scales(hs, (N + 127) >> 7, T, "hs", d)
+    else:
+        H = _out(H, (T, N), out_dtype, "H", d, dev)
+    _call("mobi_fp8_gated", d, stream, xp, ldx, xsp, T, K, gp, ldg, gsp, up, ldu, usp, N, _ACT[act], dt, H.data_ptr(),
+          _matrix(H, "H", d)[2], hsp)
+    return (H, hs) if dt == 3 else H
+
+
+def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+              eps: float = 1e-6, kind: str = "rms", block: torch.Tensor | None = None, post: str = "none",
+              post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None,
+              post_eps: float | None = None, gate: torch.Tensor | None = None, scale: float = 1.0,
+              unit_offset: bool = False, out_dtype=torch.bfloat16, N: torch.Tensor | None = None,
+              n_scale: torch.Tensor | None = None, R: torch.Tensor | None = None, stream=None):
+    """The step between two blocks in one pass: r = x + scale * gate * post(block), n = kind(r) * weight + bias.
+
+    x [T, D] is the residual stream, block [T, D] the block's output (None: a plain norm of x), gate anything that
+    broadcasts to [T, D]; kind and post are "rms", "layer" or "none". -> (n, r), or n alone without a block; n is
+    a pair (codes, scales) for out_dtype torch.float8_e4m3fn. R=x updates the residual stream in place."""
+    T, D, ldx = _matrix(x, "x")
+    d, dev = x.get_device(), x.device
+    xdt, odt = _DT.get(x.dtype, 3), _DT.get(out_dtype)
+    if xdt == 3 or odt is None:
+        raise ValueError("x must be fp32, bf16 or fp16, out_dtype one of these or e4m3")
+    if kind not in _NORM or post not in _NORM:
+        raise ValueError('kind and post must be "rms", "layer" or "none"')
+    wdt = None
+    for w in (weight, bias, post_weight, post_bias):
+        if w is not None:
+            if wdt is not None and w.dtype is not wdt:
+                raise ValueError("the weights and biases must have one type")
+            wdt = w.dtype
+    wdt = 0 if wdt is None else _DT.get(wdt, 3)
+    if wdt == 3:
+        raise ValueError("the weights and biases must be fp32, bf16 or fp16")
+    a = NormArgs()
+    a.x, a.T, a.D, a.ldx, a.x_dtype, a.weight_dtype, a.out_dtype = x.data_ptr(), T, D, ldx, xdt, wdt, odt
+    a.weight, a.bias = _vector(weight, D, "weight", d), _vector(bias, D, "bias", d)
+    a.kind, a.eps, a.unit_offset = _NORM[kind], eps, int(unit_offset)
+    if block is not None:
+        if block.shape != x.shape:
+            raise ValueError("block must have the shape of x")
+        a.ldb = _matrix(block, "block", d)[2]
+        a.block, a.block_dtype = block.data_ptr(), _DT.get(block.dtype, 3)
+        if a.block_dtype == 3:
+            raise ValueError("block must be fp32, bf16 or fp16")
+        a.post, a.post_eps, a.scale = _NORM[post], eps if post_eps is None else post_eps, scale
+        a.post_weight = _vector(post_weight, D, "post_weight", d)
+        a.post_bias = _vector(post_bias, D, "post_bias", d)
+        if gate is not None:
+            _on(gate, "gate", d)
+            a.gate_dtype = _DT.get(gate.dtype, 3)
+            if a.gate_dtype == 3:
+                raise ValueError("gate must be fp32, bf16 or fp16")
+            a.gate_st, a.gate_sd = gate.expand(T, D).stride()
+            a.gate = gate.data_ptr()
+        R = _out(R, (T, D), x.dtype, "R", d, dev)
+        a.r_out, a.ldr = R.data_ptr(), _matrix(R, "R", d)[2]
+    elif R is not None or gate is not None or post_weight is not None or post_bias is not None:
+        raise ValueError("R, gate and the post norm's weights need a block")
+    if odt == 3:
+        N = _codes(T, D, dev) if N is None else _out(N, (T, D), E4M3, "N", d, dev)
+        if n_scale is None:
+            n_scale = torch.empty(((D + 127) >> 7, T), dtype=torch.float32, device=dev)
+        a.n_scale = _scales(n_scale, (D + 127) >> 7, T, "n_scale", d)
+    else:
+        N = _out(N, (T, D), out_dtype, "N", d, dev)
+    a.n_out, a.ldn = N.data_ptr(), _matrix(N, "N", d)[2]
+    _call("mobi_norm", d, stream, ctypes.addressof(a))
+    n = (N, n_scale) if odt == 3 else N
+    return n if block is None else (n, R)
+
+
+def mobi_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, temperature: float = 1.0,
+                  top_k: int = 0, entropy: bool = True, stream=None):
+    """Scoring of logits [T, V] (fp32, bf16 or fp16) -> (logprob [T] of the int64 targets, entropy [T],
+    top_logprob [T, top_k], top_index int32 [T, top_k]); logprob is None without targets, entropy without
+    entropy=True. A negative target is ignored (log probability 0); one >= V is reported by mobi_sync_check."""
+    T, V, ld = _matrix(logits, "logits")
+    d, dev = logits.get_device(), logits.device
+    dt = _DT.get(logits.dtype, 3)
+    if dt == 3:
+        raise ValueError("logits must be fp32, bf16 or fp16")
+    tp = _vector(targets, T, "targets", d, torch.int64)
+    k = int(top_k)
+    f32 = torch.float32
+    lp = None if tp is None else torch.empty(T, dtype=f32, device=dev)
+    en = torch.empty(T, dtype=f32, device=dev) if entropy else None
+    top = torch.empty((T, max(k, 0)), dtype=f32, device=dev)
+    idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    _call("mobi_logprobs", d, stream, logits.data_ptr(), dt, T, V, ld, tp, temperature, k,
+          None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(), top.data_ptr(),
+          idx.data_ptr())
+    return lp, en, top, idx

@@ -211,6 +211,24 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t c
   return make_tmap(map, base, elem_bytes, 2, dims, strides, box, swizzle_bytes);
 }
 
+bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                  uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) {
+    note_message("cuTensorMapEncodeTiled is not available");
+    return false;
+  }
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled: CUresult %d (%llu x %llu bytes, pitch %llu)",
+             (int)r, (unsigned long long)rows, (unsigned long long)cols, (unsigned long long)pitch);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mobi
 
 using namespace mobi;
@@ -696,6 +714,10 @@ mobi_status mobi_sync_check(void* stream) {
   if (h.error & kErrTimeout) {
     snprintf(g_last_error, sizeof g_last_error, "a bounded wait ran out in a kernel (wait site 0x%x)", h.where);
     return MOBI_ERR_TIMEOUT;
+  }
+  if (!(h.error & kErrInputRange)) {
+    note_message("a target of mobi_logprobs is outside the vocabulary");
+    return MOBI_ERR_INVALID_ARG;  // kErrTargetRange
   }
   note_message("an activation of a decode call (T <= 16) had |x| >= 2^31");
   return MOBI_ERR_INVALID_ARG;  // kErrInputRange

@@ -1,0 +1,715 @@
+// mobi_fp8.cu — products of e4m3 operands with one fp32 scale for each block of
+// 128 values along K (activations: 1 x 128, weights: 128 x 128), on tcgen05:
+//
+//   mobi_fp8_gemm    y[t,n] = sum_b xs[b,t] ws[b,n/128] sum_{k in b} x[t,k] w[n,k]
+//   mobi_fp8_gated   h[t,n] = act(g[t,n]) u[t,n], g and u as above with their own weights,
+//                    optionally requantised to e4m3 in blocks of 128 columns
+//
+// Products of e4m3 values are exact in fp32; one block's sum is accumulated by
+// the tensor core in TMEM and promoted, acc = fma(xs ws, D, acc), in fp32
+// registers before the next block's sum replaces it. Nothing is rounded to
+// fewer bits before the output.
+//
+// Two kernels. "wide" puts tokens on the TMEM lanes (tile 128 tokens x 256
+// output columns, or 128 gate + 128 up columns) and keeps a persistent CTA on
+// every SM; the promotion's scale is one register per thread. "narrow" puts
+// weight rows on the lanes (128 rows x 16..128 tokens), so that one token costs
+// a 16-wide tile and not a 128-wide one, and splits K over a cluster whose CTAs
+// add their sums through distributed shared memory in rank order.
+//
+// All mbarrier waits are bounded; on a timeout the kernel records the error,
+// drains its copies and MMAs in flight, frees TMEM and returns.
+#include <cstdint>
+
+#include "mobi_device.cuh"
+#include "mobi_host.h"
+
+namespace mobi {
+
+namespace f8 {
+constexpr int BK = 128;                     // one scale block along K = one 128-byte swizzled row
+constexpr uint32_t kTileBytes = 128 * BK;   // 128 rows of one block
+constexpr int kEpiWarps = 8;
+
+enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3 };
+
+__device__ __forceinline__ float activate(float g, int act) {
+  switch (act) {
+    case kSilu: return g / (1.0f + expf(-g));
+    case kGelu: return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    case kGeluTanh: return 0.5f * g * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * g * g, g, g)));
+    default: return g > 0.0f ? g : (g == g ? 0.0f : g);
+  }
+}
+
+struct Out {
+  void* y;          // [T][ld] of `type`
+  float* scale;     // e4m3: [ceil(N/128)][T]
+  int64_t ld;
+  int type;         // MOBI_F32, MOBI_BF16, MOBI_F16, MOBI_E4M3
+  int vec;          // rows may be written 16 bytes at a time
+};
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+}  // namespace f8
+
+// ---- wide: tokens on lanes ---------------------------------------------------------
+
+namespace f8w {
+constexpr int ST = 4;                       // pipeline stages (one block of K each)
+constexpr int BN = 256;                     // weight rows per tile: 256, or 128 gate + 128 up
+constexpr uint32_t kABytes = f8::kTileBytes, kBBytes = 2 * f8::kTileBytes;
+constexpr int kThreads = 12 * 32;           // 0 producer, 1 MMA, 2-3 set-up only, 4-11 epilogue
+constexpr int kGroupM = 16;                 // token tiles swept together over the weight tiles (L2 reuse)
+
+struct Smem {
+  uint8_t a[ST][kABytes];                   // 1024-byte aligned (offset 0)
+  uint8_t b[ST][kBBytes];
+  uint8_t out[f8::kEpiWarps][32 * 128];     // per warp: 32 rows x 128 bytes, 16-byte chunk j of row r at j ^ (r & 7)
+  uint32_t rowmax[2][128];                  // e4m3 output: |h| maxima of a row's two halves
+  uint64_t full[ST], empty[ST], d_full[2], d_empty[2], drain;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+
+// Tile index -> (token tile, weight tile): kGroupM token tiles at a time, weight
+// tiles outermost within them, so CTAs that run together share both operands.
+__device__ __forceinline__ void tile_at(int64_t i, int64_t n_mt, int64_t n_nt, int64_t* m, int64_t* n) {
+  const int64_t per = kGroupM * n_nt, g = i / per, r = i % per;
+  const int64_t left = n_mt - g * kGroupM, rows = left < kGroupM ? left : kGroupM;
+  *m = g * kGroupM + r % rows;
+  *n = r / rows;
+}
+
+// Writes a warp's staged 32 rows (row pitch 128 bytes, `cols` elements of ES
+// bytes each) to y[t0 + row][n0 + col], clipped to T and N.
+template <int ES, int COLS>
+__device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* y, int64_t ld, int64_t t0, int64_t T,
+                                           int64_t n0, int64_t N, bool vec, int lane) {
+  constexpr int CH = COLS * ES / 16, EC = 16 / ES;  // 16-byte chunks of a row, elements of a chunk
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int row = (i * 32 + lane) / CH, ch = lane % CH;
+    const int64_t t = t0 + row, n = n0 + ch * EC;
+    if (t >= T || n >= N) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + 16 * (ch ^ (row & 7)));
+    uint8_t* p = y + (t * ld + n) * ES;
+    if (vec && n + EC <= N) {
+      *reinterpret_cast<uint4*>(p) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < EC; ++e)
+        if (n + e < N) {
+          if (ES == 4) reinterpret_cast<uint32_t*>(p)[e] = w[e];
+          if (ES == 2) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+          if (ES == 1) p[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+        }
+    }
+  }
+}
+
+// One warp's 32 rows x NC columns (acc, a row per lane) to y, through its staging rows.
+template <int NC>
+__device__ __forceinline__ void write_out(const float (&v)[NC], uint8_t* stage, const f8::Out& o, int64_t t0, int64_t T,
+                                          int64_t n0, int64_t N, int lane) {
+  uint8_t* y = static_cast<uint8_t*>(o.y);
+  uint8_t* row = stage + lane * 128;
+  if (o.type == MOBI_F32) {
+#pragma unroll
+    for (int c = 0; c < NC / 32; ++c) {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(row + 16 * (j ^ (lane & 7))) =
+            make_float4(v[32 * c + 4 * j], v[32 * c + 4 * j + 1], v[32 * c + 4 * j + 2], v[32 * c + 4 * j + 3]);
+      __syncwarp();
+      store_rows<4, 32>(stage, y, o.ld, t0, T, n0 + 32 * c, N, o.vec, lane);
+    }
+  } else {
+    const bool half = o.type == MOBI_F16;
+#pragma unroll
+    for (int c = 0; c < NC / 64; ++c) {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = v[64 * c + 8 * j + 2 * e], hi = v[64 * c + 8 * j + 2 * e + 1];
+          w[e] = half ? f8::pack_f16(lo, hi) : f8::pack_bf16(lo, hi);
+        }
+        *reinterpret_cast<uint4*>(row + 16 * (j ^ (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      store_rows<2, 64>(stage, y, o.ld, t0, T, n0 + 64 * c, N, o.vec, lane);
+    }
+  }
+}
+}  // namespace f8w
+
+template <bool GATED>
+__global__ void __launch_bounds__(f8w::kThreads, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_u, const float* xs,
+                    const float* ws, const float* us, int64_t T, int64_t N, int nkb, int act,
+                    f8::Out out, DeviceStatus* st, uint64_t limit) {
+  using namespace f8w;
+  constexpr int TN = GATED ? 128 : 256;  // output columns of a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int32_t* abort_flag = &sm.abort_flag;
+  const int64_t n_mt = (T + 127) / 128, n_nt = (N + TN - 1) / TN, ntiles = n_mt * n_nt;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) { mbar_init(&sm.full[i], 1); mbar_init(&sm.empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&sm.d_full[i], 1); mbar_init(&sm.d_empty[i], f8::kEpiWarps); }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // 384 threads x 168 registers at launch = 128 x 56 + 256 x 224.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
+      // ---- TMA producer ----
+      prefetch_tmap(&tm_x);
+      prefetch_tmap(&tm_w);
+      if (GATED) prefetch_tmap(&tm_u);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+        int64_t m, n;
+        tile_at(i, n_mt, n_nt, &m, &n);
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const uint32_t s = it % ST;
+          if (!(ok = mbar_wait_abort(&sm.empty[s], ((it / ST) & 1) ^ 1, limit, st, 0x501, abort_flag))) break;
+          mbar_arrive_expect_tx(&sm.full[s], kABytes + kBBytes);
+          tma_load_2d(&sm.a[s][0], &tm_x, kb * f8::BK, (int)(m * 128), &sm.full[s]);
+          tma_load_2d(&sm.b[s][0], &tm_w, kb * f8::BK, (int)(n * TN), &sm.full[s]);
+          if (GATED) tma_load_2d(&sm.b[s][f8::kTileBytes], &tm_u, kb * f8::BK, (int)(n * TN), &sm.full[s]);
+        }
+      }
+      for (uint32_t j = (it > ST ? it - ST : 0); j < it; ++j)  // every copy lands before the CTA may exit
+        mbar_wait(&sm.full[j % ST], (j / ST) & 1, kDefaultWaitLimit, st, 0x5F1);
+    } else if (warp == 1 && lane == 0) {
+      // ---- MMA issuer ----
+      const uint32_t idesc = idesc_e4m3(128, BN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const uint32_t s = it % ST, db = it & 1;
+          if (!(ok = mbar_wait_abort(&sm.full[s], (it / ST) & 1, limit, st, 0x511, abort_flag))) break;
+          if (!(ok = mbar_wait_abort(&sm.d_empty[db], ((it >> 1) & 1) ^ 1, limit, st, 0x512, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t a = smem_addr(&sm.a[s][0]), b = smem_addr(&sm.b[s][0]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_f8(tmem + db * BN, desc_sw128(a + 32 * k), desc_sw128(b + 32 * k), idesc, k > 0);
+          mma_commit(&sm.empty[s]);
+          mma_commit(&sm.d_full[db]);
+        }
+      }
+      mma_commit(&sm.drain);  // every MMA issued is done before TMEM is released
+      mbar_wait(&sm.drain, 0, kDefaultWaitLimit, st, 0x5F2);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---- epilogue: promotion by the block scales, then the output ----
+    const int e = warp - 4, q = warp & 3, half = e >> 2;
+    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
+    uint8_t* stage = sm.out[e];
+    uint32_t it = 0;
+    bool ok = true;
+    // After an abort a warp still walks its tiles, without waits on mbarriers or
+    // stores, since the other half of its rows may stand at their barrier.
+    for (int64_t i = blockIdx.x; i < ntiles; i += gridDim.x) {
+      int64_t m, n;
+      tile_at(i, n_mt, n_nt, &m, &n);
+      const int64_t trow = m * 128 + 32 * q, t = trow + lane, tc = t < T ? t : T - 1;
+      const int64_t nblk = (N + 127) / 128;
+      // Weight blocks of this warp's columns. Plain: columns 128 half.. of the
+      // tile are block 2 n + half (clamped when the tile ends before it).
+      // Gated: columns 64 half.. of the gate and of the up tile, both block n.
+      const int64_t wb = GATED ? n : (2 * n + half < nblk ? 2 * n + half : nblk - 1);
+      float2 acc[64];  // plain: 128 columns; gated: 64 gate columns, then the same 64 up columns
+#pragma unroll
+      for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
+      float sx = *(xs + tc), sw = *(ws + wb), su = GATED ? *(us + wb) : 0.0f;
+      for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
+        const float s0 = sx * sw, s1 = GATED ? sx * su : s0;
+        if (kb + 1 < nkb) {
+          sx = *(xs + (int64_t)(kb + 1) * T + tc);
+          sw = *(ws + (int64_t)(kb + 1) * nblk + wb);
+          if (GATED) su = *(us + (int64_t)(kb + 1) * nblk + wb);
+        }
+        const uint32_t db = it & 1;
+        if (!(ok = mbar_wait_abort(&sm.d_full[db], (it >> 1) & 1, limit, st, 0x521, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + lane_addr + db * BN;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          const int col = GATED ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
+          tmem_ld32(d + col, r);
+          tmem_ld_wait();
+          const float s = GATED && c >= 2 ? s1 : s0;
+          const float2 s2 = make_float2(s, s);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = __ffma2_rn(s2, make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
+                                         acc[16 * c + j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.d_empty[db]);
+      }
+      if constexpr (!GATED) {
+        if (ok) write_out<128>(reinterpret_cast<const float(&)[128]>(acc), stage, out, trow, T, n * 256 + 128 * half, N, lane);
+      } else {
+        float h[64];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          h[2 * c] = f8::activate(acc[c].x, act) * acc[32 + c].x;
+          h[2 * c + 1] = f8::activate(acc[c].y, act) * acc[32 + c].y;
+        }
+        const int64_t n0 = n * 128 + 64 * half;
+        if (out.type != MOBI_E4M3) {
+          if (ok) write_out<64>(h, stage, out, trow, T, n0, N, lane);
+        } else {
+          // Block maximum of the row: this thread's 64 columns and, through
+          // shared memory, the other half's. Columns past N are exact zeros
+          // (zero-filled weights give g = u = 0).
+          uint32_t a = 0;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) a = max(a, abs_bits(h[c]));
+          sm.rowmax[half][32 * q + lane] = a;
+          f8::named_barrier(1 + q, 64);
+          a = max(a, sm.rowmax[half ^ 1][32 * q + lane]);
+          f8::named_barrier(1 + q, 64);  // read before the next tile writes it
+          if (!ok) continue;
+          const float s = block_scale(a), r = 1.0f / s;
+          if (half == 0 && t < T) out.scale[n * T + t] = s;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = e4m3x2(h[16 * j + 4 * k] * r, h[16 * j + 4 * k + 1] * r) |
+                     (e4m3x2(h[16 * j + 4 * k + 2] * r, h[16 * j + 4 * k + 3] * r) << 16);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * (j ^ (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+          store_rows<1, 64>(stage, static_cast<uint8_t*>(out.y), out.ld, trow, T, n0, N, out.vec, lane);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- narrow: weight rows on lanes, K split over a cluster ------------------------------
+
+namespace f8n {
+constexpr int kThreads = 10 * 32;  // 0-7 epilogue, 8 producer, 9 MMA
+
+template <bool GATED, int BN>
+struct Cfg {
+  static constexpr int MATS = GATED ? 2 : 1;
+  static constexpr int COLS = MATS * BN;                     // accumulator columns of one block's sums
+  static constexpr int HC = COLS / 2;                        // of which an epilogue warp takes half
+  static constexpr int DST = COLS <= 32 ? 4 : 2;             // accumulator buffers in TMEM
+  static constexpr int TMEM = DST * COLS < 32 ? 32 : DST * COLS;
+  static constexpr uint32_t kWBytes = MATS * f8::kTileBytes, kXBytes = BN * f8::BK;
+  static constexpr uint32_t kStage = kWBytes + kXBytes;
+  // Stages: as many bytes in flight as one (BN >= 64) or two CTAs of an SM can hold.
+  static constexpr int ST = GATED ? (BN == 64 ? 3 : 2) : (BN == 16 ? 5 : (BN == 64 ? 6 : 4));
+  static constexpr int kPerSm = BN <= 32 ? 2 : 1;            // CTAs that share an SM
+  static_assert(HC >= 8 && HC <= 64 && TMEM <= 512 && (TMEM & (TMEM - 1)) == 0, "tile");
+};
+
+template <bool GATED, int BN>
+struct Smem {
+  using C = Cfg<GATED, BN>;
+  uint8_t w[C::ST][C::kWBytes];          // 1024-byte aligned (offset 0)
+  uint8_t x[C::ST][C::kXBytes];
+  float red[C::COLS * 128];              // [source rank][owned column][row]: the cluster's sums of the owned tokens
+  float scale[f8::kEpiWarps][2][64];     // per warp: block scales of its columns, double-buffered
+  uint32_t colmax[2][2][4];
+  uint64_t full[C::ST], empty[C::ST], d_full[C::DST], d_empty[C::DST], drain;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+}  // namespace f8n
+
+template <bool GATED, int BN>
+__global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
+    fp8_narrow_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_u, const float* xs,
+                      const float* ws, const float* us, int64_t T, int64_t N, int nkb,
+                      int csize, int act, f8::Out out, DeviceStatus* st, uint64_t limit) {
+  using CF = f8n::Cfg<GATED, BN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  f8n::Smem<GATED, BN>& sm = *reinterpret_cast<f8n::Smem<GATED, BN>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int32_t* abort_flag = &sm.abort_flag;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int64_t n0 = (int64_t)(blockIdx.x / csize) * 128, t0 = (int64_t)blockIdx.y * BN;
+  const int kb0 = (int)((int64_t)nkb * rank / csize), kb1 = (int)((int64_t)nkb * (rank + 1) / csize);
+  const int64_t nblk = (N + 127) / 128, wb = n0 / 128;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < CF::ST; ++i) { mbar_init(&sm.full[i], 1); mbar_init(&sm.empty[i], 1); }
+    for (int i = 0; i < CF::DST; ++i) { mbar_init(&sm.d_full[i], 1); mbar_init(&sm.d_empty[i], f8::kEpiWarps); }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&sm.tmem_base, CF::TMEM);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  // Every CTA of the cluster runs before its shared memory is written (waited for below).
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  constexpr int NPER = CF::HC < 32 ? 1 : CF::HC / 32;  // scales a lane fetches
+  float2 acc[CF::HC / 2];
+#pragma unroll
+  for (int c = 0; c < CF::HC / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+  const int half = warp >> 2, q = warp & 3;
+  const int mat = GATED ? half : 0, j0 = GATED ? 0 : half * CF::HC;  // matrix and first token of this warp's columns
+
+  if (warp == 8) {
+    if (lane == 0) {
+      // ---- TMA producer ----
+      uint32_t it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % CF::ST;
+        if (!mbar_wait_abort(&sm.empty[s], ((it / CF::ST) & 1) ^ 1, limit, st, 0x531, abort_flag)) break;
+        mbar_arrive_expect_tx(&sm.full[s], CF::kStage);
+        tma_load_2d(&sm.w[s][0], &tm_w, kb * f8::BK, (int)n0, &sm.full[s]);
+        if (GATED) tma_load_2d(&sm.w[s][f8::kTileBytes], &tm_u, kb * f8::BK, (int)n0, &sm.full[s]);
+        tma_load_2d(&sm.x[s][0], &tm_x, kb * f8::BK, (int)t0, &sm.full[s]);
+      }
+      for (uint32_t j = (it > CF::ST ? it - CF::ST : 0); j < it; ++j)
+        mbar_wait(&sm.full[j % CF::ST], (j / CF::ST) & 1, kDefaultWaitLimit, st, 0x5F3);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---- MMA issuer ----
+      constexpr uint32_t idesc = idesc_e4m3(128, BN);
+      uint32_t it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % CF::ST, db = it % CF::DST;
+        if (!mbar_wait_abort(&sm.full[s], (it / CF::ST) & 1, limit, st, 0x541, abort_flag)) break;
+        if (!mbar_wait_abort(&sm.d_empty[db], ((it / CF::DST) & 1) ^ 1, limit, st, 0x542, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t w = smem_addr(&sm.w[s][0]), x = smem_addr(&sm.x[s][0]);
+#pragma unroll
+        for (int mt = 0; mt < CF::MATS; ++mt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_f8(tmem + db * CF::COLS + mt * BN, desc_sw128(w + mt * f8::kTileBytes + 32 * k),
+                      desc_sw128(x + 32 * k), idesc, k > 0);
+        mma_commit(&sm.empty[s]);
+        mma_commit(&sm.d_full[db]);
+      }
+      mma_commit(&sm.drain);
+      mbar_wait(&sm.drain, 0, kDefaultWaitLimit, st, 0x5F4);
+    }
+  } else {
+    // ---- epilogue: promotion; a lane fetches some of the warp's column scales a block ahead ----
+    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
+    const float* wsc = mat ? us : ws;
+    int64_t tok[NPER];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const int64_t t = t0 + j0 + lane % CF::HC + 32 * i;
+      tok[i] = t < T ? t : T - 1;
+    }
+    float nx[NPER], nw;
+    nw = *(wsc + (int64_t)kb0 * nblk + wb);
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) nx[i] = *(xs + (int64_t)kb0 * T + tok[i]);
+    uint32_t it = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      float* sc = sm.scale[warp][it & 1];
+#pragma unroll
+      for (int i = 0; i < NPER; ++i)
+        if (CF::HC >= 32 || lane < CF::HC) sc[lane + 32 * i] = nx[i] * nw;
+      if (kb + 1 < kb1) {
+        nw = *(wsc + (int64_t)(kb + 1) * nblk + wb);
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) nx[i] = *(xs + (int64_t)(kb + 1) * T + tok[i]);
+      }
+      __syncwarp();
+      const uint32_t db = it % CF::DST;
+      if (!mbar_wait_abort(&sm.d_full[db], (it / CF::DST) & 1, limit, st, 0x551, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + lane_addr + db * CF::COLS + half * CF::HC;
+      constexpr int LC = CF::HC < 32 ? CF::HC : 32;  // columns per TMEM load
+#pragma unroll
+      for (int c = 0; c < CF::HC / LC; ++c) {
+        uint32_t r[LC];
+        if constexpr (LC == 8) tmem_ld8(d, r);
+        if constexpr (LC == 16) tmem_ld16(d, r);
+        if constexpr (LC == 32) tmem_ld32(d + 32 * c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < LC / 4; ++j) {
+          const float4 s4 = *reinterpret_cast<const float4*>(&sc[LC * c + 4 * j]);
+          float2* a = &acc[LC / 2 * c + 2 * j];
+          a[0] = __ffma2_rn(make_float2(s4.x, s4.y),
+                            make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), a[0]);
+          a[1] = __ffma2_rn(make_float2(s4.z, s4.w),
+                            make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), a[1]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.d_empty[db]);
+    }
+  }
+
+  // The cluster's sums: CTA r owns tokens [r BN / csize, (r + 1) BN / csize) of
+  // the tile; every CTA writes its sums of them into r's shared memory, and r
+  // adds them in rank order (the result does not depend on who finishes first).
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  const int tpc = BN / csize;
+  if (warp < 8) {
+    const uint32_t red = smem_addr(&sm.red[0]);
+#pragma unroll
+    for (int c = 0; c < CF::HC; ++c) {
+      const int j = j0 + c, owner = j / tpc, slot = mat * tpc + j % tpc;
+      const uint32_t local = red + (uint32_t)((((int)rank * CF::MATS * tpc + slot) * 128 + 32 * q + lane) * 4);
+      uint32_t remote;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(owner));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"((c & 1) ? acc[c >> 1].y : acc[c >> 1].x)
+                   : "memory");
+    }
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+
+  if (warp < 8) {
+    const int row = threadIdx.x & 127;
+    const int64_t n = n0 + row;
+    const int per = CF::MATS * tpc * 128;
+    for (int tl = half; tl < tpc; tl += 2) {  // tokens of this CTA, alternating between the two groups of 128 threads
+      const int64_t t = t0 + (int64_t)rank * tpc + tl;
+      if (t >= T) break;
+      float v = 0.0f, u = 0.0f;
+      for (int c = 0; c < csize; ++c) {
+        v += sm.red[c * per + tl * 128 + row];
+        if (GATED) u += sm.red[c * per + (tpc + tl) * 128 + row];
+      }
+      if (GATED) v = f8::activate(v, act) * u;
+      if (GATED && out.type == MOBI_E4M3) {
+        uint32_t a = __reduce_max_sync(0xffffffffu, abs_bits(v));
+        uint32_t* cm = sm.colmax[half][(tl >> 1) & 1];
+        if (lane == 0) cm[q] = a;
+        f8::named_barrier(1 + half, 128);
+        a = max(max(cm[0], cm[1]), max(cm[2], cm[3]));
+        const float s = block_scale(a), r = 1.0f / s;
+        if (row == 0) out.scale[wb * T + t] = s;
+        if (n < N) static_cast<uint8_t*>(out.y)[t * out.ld + n] = (uint8_t)e4m3x2(v * r, 0.0f);
+      } else if (n < N) {
+        const int64_t at = t * out.ld + n;
+        if (out.type == MOBI_F32) static_cast<float*>(out.y)[at] = v;
+        else if (out.type == MOBI_BF16) static_cast<__nv_bfloat16*>(out.y)[at] = __float2bfloat16_rn(v);
+        else static_cast<__half*>(out.y)[at] = __float2half_rn(v);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, CF::TMEM);
+  }
+}
+
+// ---- host side ---------------------------------------------------------------------
+
+struct Fp8Job {
+  const void *X, *W, *U;
+  const float *xs, *ws, *us;
+  int64_t ldx, ldw, ldu, T, N, K;
+  f8::Out out;
+  int act;
+};
+
+// Which kernel and, for the narrow one, the token tile and the cluster.
+struct Fp8Plan {
+  bool wide;
+  int bn, csize;
+};
+
+static Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
+  Fp8Plan p;
+  const int64_t nkb = (K + 127) / 128, nt = (N + 127) / 128;
+  const int64_t wide_tiles = ((T + 127) / 128) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  p.wide = T > 128 && 2 * wide_tiles >= sms;
+  p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || gated ? 64 : 128));
+  const int64_t tiles = nt * ((T + p.bn - 1) / p.bn);
+  const int64_t room = (p.bn <= 32 ? 2 : 1) * (int64_t)sms;
+  p.csize = 1;
+  while (p.csize < 8 && tiles * p.csize * 2 <= room && nkb >= 2 * p.csize) p.csize *= 2;
+  return p;
+}
+
+template <bool GATED, int BN>
+static cudaError_t launch_narrow(const Fp8Job& j, const Fp8Plan& p, const CUtensorMap& mx, const CUtensorMap& mw,
+                                 const CUtensorMap& mu, cudaStream_t stream, DeviceStatus* st) {
+  constexpr int smem = (int)sizeof(f8n::Smem<GATED, BN>) + 1024;
+  static_assert(smem <= 232448, "shared memory");
+  cudaError_t e = set_smem((const void*)fp8_narrow_kernel<GATED, BN>, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t nt = (j.N + 127) / 128, tt = (j.T + BN - 1) / BN;
+  e = launch_dependent(fp8_narrow_kernel<GATED, BN>, dim3((unsigned)(nt * p.csize), (unsigned)tt), f8n::kThreads, smem,
+                       p.csize, stream, mx, mw, mu, j.xs, j.ws, j.us, j.T, j.N, (int)((j.K + 127) / 128), p.csize,
+                       j.act, j.out, st, wait_limit());
+  return note_error("fp8 narrow launch", e);
+}
+
+template <bool GATED>
+static cudaError_t launch_fp8(const Fp8Job& j, cudaStream_t stream) {
+  cudaError_t e;
+  DeviceStatus* st = device_status(&e);
+  if (!st) return e;
+  const int sms = num_sms();
+  const Fp8Plan p = fp8_plan(j.T, j.N, j.K, GATED, sms);
+  CUtensorMap mx, mw, mu = {};
+  const uint32_t rows_x = p.wide ? 128 : (uint32_t)p.bn, rows_w = p.wide && !GATED ? 256 : 128;
+  if (!make_tmap_u8(&mx, j.X, (uint64_t)j.K, (uint64_t)j.T, (uint64_t)j.ldx, rows_x) ||
+      !make_tmap_u8(&mw, j.W, (uint64_t)j.K, (uint64_t)j.N, (uint64_t)j.ldw, rows_w) ||
+      (GATED && !make_tmap_u8(&mu, j.U, (uint64_t)j.K, (uint64_t)j.N, (uint64_t)j.ldu, rows_w)))
+    return cudaErrorInvalidValue;
+  if (!p.wide) {
+    switch (p.bn) {
+      case 16: return launch_narrow<GATED, 16>(j, p, mx, mw, mu, stream, st);
+      case 32: return launch_narrow<GATED, 32>(j, p, mx, mw, mu, stream, st);
+      case 64: return launch_narrow<GATED, 64>(j, p, mx, mw, mu, stream, st);
+      default:
+        if constexpr (!GATED) return launch_narrow<false, 128>(j, p, mx, mw, mu, stream, st);
+        return cudaErrorInvalidValue;
+    }
+  }
+  constexpr int smem = (int)sizeof(f8w::Smem) + 1024;
+  static_assert(smem <= 232448, "shared memory");
+  e = set_smem((const void*)fp8_wide_kernel<GATED>, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((j.T + 127) / 128) * ((j.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
+  e = launch_dependent(fp8_wide_kernel<GATED>, dim3((unsigned)(tiles < sms ? tiles : sms)), f8w::kThreads, smem, 1,
+                       stream, mx, mw, mu, j.xs, j.ws, j.us, j.T, j.N, (int)((j.K + 127) / 128), j.act, j.out, st,
+                       wait_limit());
+  return note_error("fp8 wide launch", e);
+}
+
+namespace {
+constexpr int64_t kMaxDim = int64_t(1) << 28;
+
+bool aligned(const void* p, int a) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(a - 1)) == 0; }
+
+// An e4m3 operand [rows][K] with pitch ld and its scales.
+mobi_status check_operand(const void* Q, int64_t ld, int64_t K, const float* s) {
+  if (!Q || !s || ld < K) return MOBI_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || ld % 16 != 0 || !aligned(s, 4)) return MOBI_ERR_MISALIGNED;
+  return MOBI_OK;
+}
+
+mobi_status check_sizes(int64_t T, int64_t N, int64_t K) {
+  if (T < 0 || N < 0 || K < 0) return MOBI_ERR_INVALID_ARG;
+  if (T > kMaxDim || N > kMaxDim || K > kMaxDim) return MOBI_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && N > 0 && K == 0) return MOBI_ERR_UNSUPPORTED_SHAPE;
+  return MOBI_OK;
+}
+
+int dtype_bytes(int t) { return t == MOBI_F32 ? 4 : (t == MOBI_E4M3 ? 1 : 2); }
+
+mobi_status check_out(void* y, int64_t ld, int64_t N, int type, f8::Out* o) {
+  const int es = dtype_bytes(type);
+  if (!y || ld < N) return MOBI_ERR_INVALID_ARG;
+  if (!aligned(y, es)) return MOBI_ERR_MISALIGNED;
+  *o = f8::Out{y, nullptr, ld, type, aligned(y, 16) && ld * es % 16 == 0};
+  return MOBI_OK;
+}
+}  // namespace
+
+}  // namespace mobi
+
+using namespace mobi;
+
+extern "C" {
+
+mobi_status mobi_fp8_gemm(const void* X, int64_t ldx, const float* xs, int64_t T, int64_t K, const void* W, int64_t ldw,
+                          const float* wsc, int64_t N, int out_dtype, void* Y, int64_t ldy, void* stream) {
+  clear_message();
+  if (out_dtype != MOBI_F32 && out_dtype != MOBI_BF16 && out_dtype != MOBI_F16) return MOBI_ERR_INVALID_ARG;
+  mobi_status s = check_sizes(T, N, K);
+  if (s != MOBI_OK || T == 0 || N == 0) return s;
+  Fp8Job j = {X, W, nullptr, xs, wsc, nullptr, ldx, ldw, 0, T, N, K, {}, 0};
+  if ((s = check_operand(X, ldx, K, xs)) != MOBI_OK || (s = check_operand(W, ldw, K, wsc)) != MOBI_OK ||
+      (s = check_out(Y, ldy, N, out_dtype, &j.out)) != MOBI_OK)
+    return s;
+  return status_of(launch_fp8<false>(j, static_cast<cudaStream_t>(stream)));
+}
+
+mobi_status mobi_fp8_gated(const void* X, int64_t ldx, const float* xs, int64_t T, int64_t K, const void* Wg,
+                           int64_t ldg, const float* gs, const void* Wu, int64_t ldu, const float* us, int64_t N,
+                           int act, int out_dtype, void* H, int64_t ldh, float* hs, void* stream) {
+  clear_message();
+  if (out_dtype < MOBI_F32 || out_dtype > MOBI_E4M3 || act < MOBI_ACT_SILU || act > MOBI_ACT_RELU)
+    return MOBI_ERR_INVALID_ARG;
+  mobi_status s = check_sizes(T, N, K);
+  if (s != MOBI_OK || T == 0 || N == 0) return s;
+  Fp8Job j = {X, Wg, Wu, xs, gs, us, ldx, ldg, ldu, T, N, K, {}, act};
+  if ((s = check_operand(X, ldx, K, xs)) != MOBI_OK || (s = check_operand(Wg, ldg, K, gs)) != MOBI_OK ||
+      (s = check_operand(Wu, ldu, K, us)) != MOBI_OK || (s = check_out(H, ldh, N, out_dtype, &j.out)) != MOBI_OK)
+    return s;
+  if (out_dtype == MOBI_E4M3) {
+    if (!hs) return MOBI_ERR_INVALID_ARG;
+    if (!aligned(hs, 4)) return MOBI_ERR_MISALIGNED;
+    j.out.scale = hs;
+  }
+  return status_of(launch_fp8<true>(j, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -38,6 +38,35 @@ cudaError_t set_smem(const void* func, int bytes);
 bool make_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
                   uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows, int swizzle_bytes);
 
+// 2-D tensor map over a row-major [rows][cols] array of bytes with a row pitch
+// of `pitch` bytes (a multiple of 16), box [box_rows][128], 128-byte swizzle,
+// zeros outside the array. Encoded anew on every call.
+bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                  uint32_t box_rows);
+
+// Launch as a programmatic dependent of the kernel before it (its set-up
+// overlaps that kernel's end; the kernel waits with griddepcontrol.wait before
+// it touches global memory), in clusters of `cluster` CTAs along x.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---- groups of independent small problems (one launch each step) -------------------
 //
 // Problem tables travel as __grid_constant__ kernel parameters, so a CUDA graph

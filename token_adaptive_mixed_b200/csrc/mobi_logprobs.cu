@@ -1,0 +1,452 @@
+// mobi_logprobs.cu — log probabilities of given tokens, entropy and the top
+// alternatives of rows of logits.
+//
+// With c = log2(e) / temperature, m the running maximum and w = (x - m) c:
+//   S = sum 2^w,  W = sum 2^w w     (rescaled when m grows: W <- f (W + d S), S <- f S, f = 2^d)
+//   logprob = (x_target - m) / temperature - ln S,   entropy = ln S - ln 2 * W / S
+// one pass over the row in fp32, no logarithm per element.
+//
+// Top alternatives without a second pass over the row: neighbouring threads
+// form 128 groups, and the k-th largest of the groups' maxima (k <= 32) is a bound tau
+// that at least k entries reach. Only groups whose maximum reaches it can hold
+// one, so about k/128 of the row is read again (from L2), the entries >= tau are
+// gathered and ranked. Many equal entries (a mask of the type's lowest value,
+// constant rows) would overflow the gather: then the entries above tau are
+// gathered and the first ones equal to it are found in index order; where even
+// those overflow, k searches over the whole row remain.
+//
+// Few rows: a cluster of up to eight CTAs shares a row; CTA 0 joins their
+// statistics and candidates through distributed shared memory, in rank order.
+#include <cmath>
+#include <cstdint>
+
+#include "mobi_device.cuh"
+#include "mobi_host.h"
+
+namespace mobi {
+
+namespace lp {
+
+constexpr int kThreads = 512;
+constexpr int kGroups = 128, kPerGroup = kThreads / kGroups;
+constexpr int kMaxK = 32;
+constexpr int kCap = 1024;   // gathered candidates
+constexpr float kLowest = -3.402823466e38f;
+
+struct Stat {
+  float m, s, w;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// a joined with b. A part without entries has m = kLowest, s = w = 0; f > 0 keeps 0 * infinity out of w.
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  const float da = (a.m - m) * c, db = (b.m - m) * c, fa = ex2(da), fb = ex2(db);
+  Stat r;
+  r.m = m;
+  r.s = a.s * fa + b.s * fb;
+  r.w = (fa > 0.0f ? fa * fmaf(da, a.s, a.w) : 0.0f) + (fb > 0.0f ? fb * fmaf(db, b.s, b.w) : 0.0f);
+  return r;
+}
+
+// Adds N values (fp32) to a running state.
+template <int N>
+__device__ __forceinline__ void add(Stat& a, const float (&x)[N], float c) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+  if (m > a.m) {
+    const float d = (a.m - m) * c, f = ex2(d);
+    a.w = f > 0.0f ? f * fmaf(d, a.s, a.w) : 0.0f;
+    a.s *= f;
+    a.m = m;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float w = (x[i] - a.m) * c, e = ex2(w);  // -infinity: e = 0
+    a.s += e;
+    a.w = fmaf(e, fmaxf(w, -1.0e4f), a.w);           // e = 0 long before -1e4: 0 and not 0 * infinity
+  }
+}
+
+// Candidates order by value, then the lower index first, as one integer.
+__device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
+  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 and 0 are equal
+  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return ((uint64_t)o << 32) | (uint32_t)~index;
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t o = (uint32_t)(k >> 32);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~(uint32_t)k; }
+
+// A CTA's part of a row: elements [lo, hi), of which [body, body + 16-byte chunks) are aligned.
+template <typename E>
+struct Part {
+  static constexpr int EC = 16 / sizeof(E);
+  const E* row;
+  int64_t lo, hi, body, tail;  // tail = body + EC * chunks
+  int chunks;
+
+  __device__ __forceinline__ void chunk(int i, float (&x)[EC]) const { widen(raw(i), x); }
+  __device__ __forceinline__ uint4 raw(int i) const { return reinterpret_cast<const uint4*>(row + body)[i]; }
+  static __device__ __forceinline__ void widen(const uint4& a, float (&x)[EC]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(E) == 4) {
+        x[j] = __uint_as_float(w[j]);
+      } else {
+        x[2 * j] = elem_f32<E>((uint16_t)w[j]);
+        x[2 * j + 1] = elem_f32<E>((uint16_t)(w[j] >> 16));
+      }
+    }
+  }
+  // The j-th element outside the aligned body (there are edge() of them, at most 2 (EC - 1)).
+  __device__ __forceinline__ int edge() const { return (int)(body - lo + hi - tail); }
+  __device__ __forceinline__ int64_t edge_at(int j) const {
+    return lo + j < body ? lo + j : tail + (j - (body - lo));
+  }
+};
+
+template <typename E>
+__device__ __forceinline__ Part<E> make_part(const E* row, int64_t lo, int64_t hi) {
+  constexpr int EC = Part<E>::EC;
+  Part<E> p;
+  p.row = row;
+  p.lo = lo;
+  p.hi = hi;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(row + lo);
+  int64_t head = (int64_t)((16 - a % 16) % 16 / sizeof(E));
+  if (head > hi - lo) head = hi - lo;
+  p.body = lo + head;
+  p.chunks = (int)((hi - p.body) / EC);
+  p.tail = p.body + (int64_t)p.chunks * EC;
+  return p;
+}
+
+struct Smem {
+  Stat warp[kThreads / 32];
+  float gmax[kGroups];
+  float tau;
+  int n, above, groups;
+  int list[kGroups];
+  uint64_t key[kCap];
+  uint64_t best[kThreads / 32];
+  uint64_t top[kMaxK];             // this CTA's part, in order (0: none)
+  Stat total;
+  int count[kThreads / 32];
+};
+
+__device__ __forceinline__ void push(Smem& sm, float x, int64_t i) {
+  if (*(volatile int*)&sm.n > kCap) return;  // already overflowed: the count only has to stay above kCap
+  const int at = atomicAdd(&sm.n, 1);
+  if (at < kCap) sm.key[at] = make_key(x, (uint32_t)i);
+}
+
+// Gathers the entries >= tau (strict: > tau) of the part into sm.key, sm.n their count.
+template <typename E>
+__device__ void gather(Smem& sm, const Part<E>& p, float tau, bool strict) {
+  constexpr int EC = Part<E>::EC;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) sm.n = sm.groups = 0;
+  __syncthreads();
+  if (tid < kGroups && (strict ? sm.gmax[tid] > tau : sm.gmax[tid] >= tau)) sm.list[atomicAdd(&sm.groups, 1)] = tid;
+  __syncthreads();
+  const int ng = sm.groups, per = (p.chunks + kThreads - 1) / kThreads;  // chunks of a thread
+  for (int g = warp; g < ng; g += kThreads / 32) {
+    const int base = sm.list[g] * kPerGroup;
+    for (int j = lane; j < per * kPerGroup; j += 32) {
+      const int i = (j / kPerGroup) * kThreads + base + j % kPerGroup;
+      if (i >= p.chunks) continue;
+      float x[EC];
+      p.chunk(i, x);
+#pragma unroll
+      for (int e = 0; e < EC; ++e)
+        if ((strict ? x[e] > tau : x[e] >= tau) && x[e] > -INFINITY) push(sm, x[e], p.body + (int64_t)i * EC + e);
+    }
+  }
+  if (tid < p.edge()) {
+    const int64_t i = p.edge_at(tid);
+    const float x = to_f32(p.row[i]);
+    if ((strict ? x > tau : x >= tau) && x > -INFINITY) push(sm, x, i);
+  }
+  __syncthreads();
+}
+
+// sm.top[0..k) <- the part's k largest keys in order (0 where there are fewer).
+template <typename E>
+__device__ void top_keys(Smem& sm, const Part<E>& p, int k) {
+  constexpr int EC = Part<E>::EC;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < kMaxK) sm.top[tid] = 0;
+  if (tid == 0) sm.tau = kLowest;  // fewer than k groups: every entry above -infinity
+  __syncthreads();
+  if (tid < kGroups) {  // the k-th largest group maximum (ties share a rank range; any of them is the bound)
+    const float v = sm.gmax[tid];
+    int more = 0, same = 0;
+    for (int i = 0; i < kGroups; ++i) {
+      const float o = sm.gmax[i];
+      more += o > v;
+      same += o == v;
+    }
+    if (more < k && k <= more + same) sm.tau = v;  // equal values only
+  }
+  __syncthreads();
+  const float tau = sm.tau;
+  gather(sm, p, tau, false);
+  int n = sm.n;
+  if (n > kCap) {
+    __syncthreads();
+    gather(sm, p, tau, true);
+    n = sm.n;
+    const int need = k - n;  // entries equal to tau, lowest indices first
+    if (n <= kCap && need > 0) {
+      int have = 0;
+      for (int64_t i0 = p.lo; i0 < p.hi && have < need; i0 += kThreads) {
+        const int64_t i = i0 + tid;
+        const bool eq = i < p.hi && to_f32(p.row[i]) == tau;
+        const unsigned b = __ballot_sync(0xffffffffu, eq);
+        __syncthreads();
+        if (lane == 0) sm.count[warp] = __popc(b);
+        __syncthreads();
+        int before = have, all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < warp) before += sm.count[w];
+          all += sm.count[w];
+        }
+        before += __popc(b & ((1u << lane) - 1));
+        if (eq && before < need && n + before < kCap) sm.key[n + before] = make_key(tau, (uint32_t)i);
+        have += all;
+      }
+      n += have < need ? have : need;
+      __syncthreads();
+    }
+  }
+  if (n <= kCap) {
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t key = sm.key[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += sm.key[j] > key;
+      if (rank < k) sm.top[rank] = key;
+    }
+    __syncthreads();
+    return;
+  }
+  // k searches: the largest key below the last one.
+  uint64_t last = ~0ull;
+  for (int r = 0; r < k; ++r) {
+    uint64_t best = 0;
+    for (int i = tid; i < p.chunks; i += kThreads) {
+      float x[EC];
+      p.chunk(i, x);
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        const uint64_t key = make_key(x[e], (uint32_t)(p.body + (int64_t)i * EC + e));
+        if (x[e] > -INFINITY && key < last && key > best) best = key;
+      }
+    }
+    if (tid < p.edge()) {
+      const int64_t i = p.edge_at(tid);
+      const float x = to_f32(p.row[i]);
+      const uint64_t key = make_key(x, (uint32_t)i);
+      if (x > -INFINITY && key < last && key > best) best = key;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
+      best = v > best ? v : best;
+    }
+    __syncthreads();
+    if (lane == 0) sm.best[warp] = best;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) best = sm.best[w] > best ? sm.best[w] : best;
+    if (best == 0) break;  // uniform
+    if (tid == 0) sm.top[r] = best;
+    last = best;
+  }
+  __syncthreads();
+}
+
+// An 8-byte or 4-byte word of CTA `rank`'s shared memory (the same variable there).
+template <typename V>
+__device__ __forceinline__ V remote(const V* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  V v;
+  if constexpr (sizeof(V) == 8)
+    asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 3)
+    logprobs_kernel(const E* logits, int64_t V, int64_t ld, const int64_t* targets, float temperature, int k,
+                    int csize, float* logprob, float* entropy, float* top_logprob, int32_t* top_index,
+                    DeviceStatus* st) {
+  constexpr int EC = Part<E>::EC, U = 4;  // chunks of a thread in flight
+  __shared__ Smem sm;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t t = blockIdx.x / csize;
+  const int rank = blockIdx.x % csize;
+  const E* row = logits + t * ld;
+  const float c = 1.44269504088896341f / temperature;
+  const Part<E> p = make_part(row, V * rank / csize, V * (rank + 1) / csize);
+
+  Stat a = {kLowest, 0.0f, 0.0f};
+  int i = tid;
+  for (; i + (U - 1) * kThreads < p.chunks; i += U * kThreads) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = p.raw(i + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[EC];
+      Part<E>::widen(r[u], x);
+      add<EC>(a, x, c);
+    }
+  }
+  for (; i < p.chunks; i += kThreads) {
+    float x[EC];
+    p.chunk(i, x);
+    add<EC>(a, x, c);
+  }
+  if (tid < p.edge()) {
+    const float x[1] = {to_f32(row[p.edge_at(tid)])};
+    add<1>(a, x, c);
+  }
+
+  if (k > 0) {
+    float g = a.m;
+#pragma unroll
+    for (int o = kPerGroup / 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid % kPerGroup == 0) sm.gmax[tid / kPerGroup] = g;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                    __shfl_xor_sync(0xffffffffu, a.w, o)};
+    a = join(a, b, c);
+  }
+  if (lane == 0) sm.warp[warp] = a;
+  __syncthreads();
+  if (warp == 0) {
+    a = lane < kThreads / 32 ? sm.warp[lane] : Stat{kLowest, 0.0f, 0.0f};
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                      __shfl_xor_sync(0xffffffffu, a.w, o)};
+      a = join(a, b, c);
+    }
+    if (lane == 0) sm.total = a;
+  }
+  if (k > 0) top_keys(sm, p, k);
+
+  if (csize > 1) {
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0) {
+      if (tid == 0) {
+        Stat all = sm.total;
+        for (int r = 1; r < csize; ++r) {
+          const Stat b = {remote(&sm.total.m, r), remote(&sm.total.s, r), remote(&sm.total.w, r)};
+          all = join(all, b, c);
+        }
+        sm.total = all;
+      }
+      const int n = csize * k;  // <= 8 * 32
+      if (tid < n) sm.key[tid] = remote(&sm.top[tid % k], tid / k);
+      __syncthreads();
+      const uint64_t key = tid < n ? sm.key[tid] : 0;
+      if (tid < kMaxK) sm.top[tid] = 0;
+      __syncthreads();
+      if (key) {
+        int at = 0;
+        for (int j = 0; j < n; ++j) at += sm.key[j] > key;
+        if (at < k) sm.top[at] = key;
+      }
+    }
+    // CTA 0 has read the others' shared memory before they leave.
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+  }
+  __syncthreads();
+  a = sm.total;
+  const float log_s = logf(a.s);
+  const bool empty = a.s == 0.0f;
+  if (tid < k) {
+    const uint64_t key = sm.top[tid];
+    top_index[t * k + tid] = key ? (int32_t)key_index(key) : -1;
+    top_logprob[t * k + tid] = key ? (key_value(key) - a.m) / temperature - log_s : -INFINITY;
+  }
+  if (tid == 0) {
+    if (entropy) entropy[t] = empty ? 0.0f : log_s - 0.693147180559945309f * (a.w / a.s);
+    if (targets) {
+      const int64_t y = targets[t];
+      float v = 0.0f;
+      if (y >= V) {
+        v = NAN;
+        report_error(st, kErrTargetRange, 0x601);
+      } else if (y >= 0) {
+        v = empty ? -INFINITY : (to_f32(row[y]) - a.m) / temperature - log_s;
+      }
+      logprob[t] = v;
+    }
+  }
+}
+
+template <typename E>
+static cudaError_t launch(const void* logits, int64_t T, int64_t V, int64_t ld, const int64_t* targets,
+                          float temperature, int k, float* logprob, float* entropy, float* top_logprob,
+                          int32_t* top_index, cudaStream_t stream) {
+  cudaError_t e;
+  DeviceStatus* st = device_status(&e);
+  if (!st) return e;
+  // A cluster shares a row while the rows leave SMs idle and each CTA keeps a
+  // load or more per thread.
+  int csize = 1;
+  while (csize < 8 && T * csize * 2 <= num_sms() && V >= (int64_t)csize * 2 * kThreads * Part<E>::EC) csize *= 2;
+  return launch_dependent(logprobs_kernel<E>, dim3((unsigned)(T * csize)), kThreads, 0, csize, stream,
+                          static_cast<const E*>(logits), V, ld, targets, temperature, k, csize, logprob, entropy,
+                          top_logprob, top_index, st);
+}
+
+}  // namespace lp
+
+}  // namespace mobi
+
+using namespace mobi;
+
+extern "C" mobi_status mobi_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                     const int64_t* targets, float temperature, int top_k, float* logprob,
+                                     float* entropy, float* top_logprob, int32_t* top_index, void* stream) {
+  clear_message();
+  if (T < 0 || V < 1 || dtype < MOBI_F32 || dtype > MOBI_F16 || top_k < 0 || top_k > lp::kMaxK)
+    return MOBI_ERR_INVALID_ARG;
+  if (!(temperature >= 1e-30f) || !std::isfinite(temperature)) return MOBI_ERR_INVALID_ARG;
+  if (T > (int64_t(1) << 28) || V > (int64_t(1) << 28)) return MOBI_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOBI_OK;
+  if (!logits || ld < V || (targets && !logprob) || (top_k > 0 && (!top_logprob || !top_index)))
+    return MOBI_ERR_INVALID_ARG;
+  auto off = [](const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; };
+  if (off(logits, dtype == MOBI_F32 ? 4 : 2) || off(targets, 8) || off(logprob, 4) || off(entropy, 4) ||
+      off(top_logprob, 4) || off(top_index, 4))
+    return MOBI_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const auto fn = dtype == MOBI_F32 ? lp::launch<float> : (dtype == MOBI_BF16 ? lp::launch<__nv_bfloat16> : lp::launch<__half>);
+  return status_of(note_error("logprobs launch", fn(logits, T, V, ld, targets, temperature, top_k, logprob, entropy,
+                                                    top_logprob, top_index, s)));
+}
