@@ -10,9 +10,10 @@
 // registers before the next block's sum replaces it. Nothing is rounded to
 // fewer bits before the output.
 //
-// Two kernels. "wide" puts tokens on the TMEM lanes (tile 128 tokens x 256
-// output columns, or 128 gate + 128 up columns) and keeps a persistent CTA on
-// every SM; the promotion's scale is one register per thread. "narrow" puts
+// Two kernels. "wide" puts tokens on the TMEM lanes: a persistent pair of CTAs
+// (cta_group::2) per two SMs takes tiles of 256 tokens x 256 output columns (or
+// 128 gate + 128 up columns), each CTA holding half of the tokens and half of
+// the weight rows; the promotion's scale is one register per thread. "narrow" puts
 // weight rows on the lanes (128 rows x 16..128 tokens), so that one token costs
 // a 16-wide tile and not a 128-wide one, and splits K over a cluster whose CTAs
 // add their sums through distributed shared memory in rank order.
@@ -33,12 +34,30 @@ constexpr int kEpiWarps = 8;
 
 enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3 };
 
+// silu with the fast exponential and division: each is off by a few fp32 steps
+// (the exponential's error grows with |g|, where silu vanishes or equals g).
+template <int ACT>
+__device__ __forceinline__ float activate_as(float g) {
+  if (ACT == kSilu) return __fdividef(g, 1.0f + __expf(-g));
+  if (ACT == kGelu) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+  if (ACT == kGeluTanh) return 0.5f * g * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * g * g, g, g)));
+  return g > 0.0f ? g : (g == g ? 0.0f : g);
+}
 __device__ __forceinline__ float activate(float g, int act) {
   switch (act) {
-    case kSilu: return g / (1.0f + expf(-g));
-    case kGelu: return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
-    case kGeluTanh: return 0.5f * g * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * g * g, g, g)));
-    default: return g > 0.0f ? g : (g == g ? 0.0f : g);
+    case kSilu: return activate_as<kSilu>(g);
+    case kGelu: return activate_as<kGelu>(g);
+    case kGeluTanh: return activate_as<kGeluTanh>(g);
+    default: return activate_as<kRelu>(g);
+  }
+}
+// h = act(g) u for a row's gate values (acc[0]) and up values (acc[1]); one straight run of code per activation, since it is executed once a tile.
+template <int ACT>
+__device__ __forceinline__ void gate_row(const float2 (&acc)[2][32], float (&h)[64]) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    h[2 * c] = activate_as<ACT>(acc[0][c].x) * acc[1][c].x;
+    h[2 * c + 1] = activate_as<ACT>(acc[0][c].y) * acc[1][c].y;
   }
 }
 
@@ -66,17 +85,23 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // ---- wide: tokens on lanes ---------------------------------------------------------
 
 namespace f8w {
-constexpr int ST = 4;                       // pipeline stages (one block of K each)
-constexpr int BN = 256;                     // weight rows per tile: 256, or 128 gate + 128 up
-constexpr uint32_t kABytes = f8::kTileBytes, kBBytes = 2 * f8::kTileBytes;
-constexpr int kThreads = 12 * 32;           // 0 producer, 1 MMA, 2-3 set-up only, 4-11 epilogue
-constexpr int kGroupM = 16;                 // token tiles swept together over the weight tiles (L2 reuse)
+constexpr int ST = 5;                       // pipeline stages (one block of K each)
+constexpr int BM = 256, BN = 256;           // tokens and weight rows (or 128 gate + 128 up) of a pair's tile
+constexpr uint32_t kStage = 2 * f8::kTileBytes;  // a CTA's half of either operand
+constexpr int kThreads = 12 * 32;           // 0 producer, 1 and 2 MMA, 3 scales, 4-11 epilogue
+constexpr int kGroupM = 8;                  // token tiles swept together over the weight tiles (L2 reuse)
+constexpr int kRing = 8, kAhead = 6;        // fetched scales: slots, and blocks between the fetch and the use
+constexpr uint64_t kDrainLimit = 1 << 16;   // polls while the last copies land (only an abort runs them out)
 
 struct Smem {
-  uint8_t a[ST][kABytes];                   // 1024-byte aligned (offset 0)
-  uint8_t b[ST][kBBytes];
+  uint8_t a[ST][f8::kTileBytes];            // 1024-byte aligned (offset 0)
+  uint8_t b[ST][f8::kTileBytes];
   uint8_t out[f8::kEpiWarps][32 * 128];     // per warp: 32 rows x 128 bytes, 16-byte chunk j of row r at j ^ (r & 7)
+  float xs[kRing][128];                     // fetched scales of the CTA's tokens and of the tile's two weight blocks
+  float ws[kRing][4];
+  float scale[4][2][128];                   // their products: [slot][weight block][token]
   uint32_t rowmax[2][128];                  // e4m3 output: |h| maxima of a row's two halves
+  // full and d_empty are used in the first CTA of the pair (it issues the MMAs), empty and d_full in both.
   uint64_t full[ST], empty[ST], d_full[2], d_empty[2], drain;
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -97,6 +122,17 @@ template <int ES, int COLS>
 __device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* y, int64_t ld, int64_t t0, int64_t T,
                                            int64_t n0, int64_t N, bool vec, int lane) {
   constexpr int CH = COLS * ES / 16, EC = 16 / ES;  // 16-byte chunks of a row, elements of a chunk
+  if (vec && t0 + 32 <= T && n0 + COLS <= N) {
+    const int row0 = lane / CH, ch = lane % CH;
+    uint8_t* p = y + ((t0 + row0) * ld + n0 + ch * EC) * ES;
+    const int64_t step = (32 / CH) * ld * ES;
+#pragma unroll
+    for (int i = 0; i < CH; ++i, p += step) {
+      const int row = row0 + i * (32 / CH);
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(stage + row * 128 + 16 * (ch ^ (row & 7)));
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int row = (i * 32 + lane) / CH, ch = lane % CH;
@@ -170,18 +206,23 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int32_t* abort_flag = &sm.abort_flag;
-  const int64_t n_mt = (T + 127) / 128, n_nt = (N + TN - 1) / TN, ntiles = n_mt * n_nt;
+  const uint32_t rank = cluster_rank();
+  const int64_t n_mt = (T + BM - 1) / BM, n_nt = (N + TN - 1) / TN, ntiles = n_mt * n_nt;
+  const int64_t first = blockIdx.x / 2, stride = gridDim.x / 2;  // this pair's tiles
+  const int64_t units = (ntiles - first + stride - 1) / stride * nkb;  // and their blocks (first < ntiles)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) { mbar_init(&sm.full[i], 1); mbar_init(&sm.empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&sm.d_full[i], 1); mbar_init(&sm.d_empty[i], f8::kEpiWarps); }
-    mbar_init(&sm.drain, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&sm.d_full[i], 2); mbar_init(&sm.d_empty[i], 2 * f8::kEpiWarps); }
+    mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_arrive();  // both CTAs' barriers are set up before either signals the other's
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -191,47 +232,128 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
-      // ---- TMA producer ----
+      // ---- TMA producer: this CTA's tokens and its half of the weight rows (gated: gate or up) ----
+      const CUtensorMap* tw = GATED && rank ? &tm_u : &tm_w;
+      const uint32_t full0 = map_to_rank(&sm.full[0], 0);
       prefetch_tmap(&tm_x);
-      prefetch_tmap(&tm_w);
-      if (GATED) prefetch_tmap(&tm_u);
-      uint32_t it = 0;
+      prefetch_tmap(tw);
+      uint32_t s = 0, ph = 1;
+      int64_t issued = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+      for (int64_t i = first; i < ntiles && ok; i += stride) {
         int64_t m, n;
         tile_at(i, n_mt, n_nt, &m, &n);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % ST;
-          if (!(ok = mbar_wait_abort(&sm.empty[s], ((it / ST) & 1) ^ 1, limit, st, 0x501, abort_flag))) break;
-          mbar_arrive_expect_tx(&sm.full[s], kABytes + kBBytes);
-          tma_load_2d(&sm.a[s][0], &tm_x, kb * f8::BK, (int)(m * 128), &sm.full[s]);
-          tma_load_2d(&sm.b[s][0], &tm_w, kb * f8::BK, (int)(n * TN), &sm.full[s]);
-          if (GATED) tma_load_2d(&sm.b[s][f8::kTileBytes], &tm_u, kb * f8::BK, (int)(n * TN), &sm.full[s]);
+        const int xr = (int)(m * BM) + 128 * rank, wr = (int)(n * TN) + (GATED ? 0 : 128 * rank);
+        for (int kb = 0; kb < nkb; ++kb, ++issued) {
+          if (!(ok = mbar_wait_abort(&sm.empty[s], ph, limit, st, 0x501, abort_flag))) break;
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kStage);
+          const uint32_t bar = full0 + s * 8;
+          tma_load_2d_pair(&sm.a[s][0], &tm_x, kb * f8::BK, xr, bar);
+          tma_load_2d_pair(&sm.b[s][0], tw, kb * f8::BK, wr, bar);
+          if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
-      for (uint32_t j = (it > ST ? it - ST : 0); j < it; ++j)  // every copy lands before the CTA may exit
-        mbar_wait(&sm.full[j % ST], (j / ST) & 1, kDefaultWaitLimit, st, 0x5F1);
-    } else if (warp == 1 && lane == 0) {
-      // ---- MMA issuer ----
-      const uint32_t idesc = idesc_e4m3(128, BN);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % ST, db = it & 1;
-          if (!(ok = mbar_wait_abort(&sm.full[s], (it / ST) & 1, limit, st, 0x511, abort_flag))) break;
-          if (!(ok = mbar_wait_abort(&sm.d_empty[db], ((it >> 1) & 1) ^ 1, limit, st, 0x512, abort_flag))) break;
+      // A stage's release says that its copies have landed and been read.
+      for (int j = 0; j < ST && j < issued; ++j) {
+        s = s == 0 ? ST - 1 : s - 1;
+        if (s == ST - 1) ph ^= 1;
+        mbar_wait(&sm.empty[s], ph ^ 1, kDrainLimit, st, 0x5F1);
+      }
+    } else if (warp == 1 || warp == 2) {
+      // ---- MMA issuers, for both CTAs: warp 1 takes the even blocks (D buffer 0), warp 2 the odd ones ----
+      // Issuing waits for room in the tensor pipe's short queue, a barrier check
+      // takes about 100 clocks even where it is ready, and a commit half of that:
+      // one thread alone left the pipe idle for half of the time. Each thread
+      // tests the next block's stage while it issues this one.
+      if (lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = idesc_e4m3(BM, BN);
+        const uint64_t a0 = desc_sw128(smem_addr(&sm.a[0][0])), b0 = desc_sw128(smem_addr(&sm.b[0][0]));
+        const int par = warp - 1;
+        const uint32_t d = tmem + par * BN;
+        uint32_t s = par, ph = 0, dph = 1;
+        bool have = false;
+        for (int64_t it = par; it < units; it += 2) {
+          if (!mbar_wait_abort(&sm.d_empty[par], dph, limit, st, 0x512, abort_flag)) break;
+          if (!have && !mbar_wait_abort(&sm.full[s], ph, limit, st, 0x511, abort_flag)) break;
           tc_fence_after();
-          const uint32_t a = smem_addr(&sm.a[s][0]), b = smem_addr(&sm.b[s][0]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss_f8(tmem + db * BN, desc_sw128(a + 32 * k), desc_sw128(b + 32 * k), idesc, k > 0);
-          mma_commit(&sm.empty[s]);
-          mma_commit(&sm.d_full[db]);
+          const uint32_t s0 = s;
+          const uint64_t a = a0 + s * (f8::kTileBytes / 16), b = b0 + s * (f8::kTileBytes / 16);
+          dph ^= 1;
+          s += 2;
+          if (s >= ST) {
+            s -= ST;
+            ph ^= 1;
+          }
+          have = mbar_test_wait(&sm.full[s], ph);
+          mma_ss_f8_pair<false>(d, a, b, idesc);
+          mma_ss_f8_pair<true>(d, a + 2, b + 2, idesc);
+          mma_ss_f8_pair<true>(d, a + 4, b + 4, idesc);
+          mma_ss_f8_pair<true>(d, a + 6, b + 6, idesc);
+          mma_commit_pair(&sm.d_full[par]);
+          mma_commit_pair(&sm.empty[s0]);
         }
+        mma_commit_pair_local(&sm.drain);  // every MMA issued is done before TMEM is released
+        mbar_wait(&sm.drain, 0, kDefaultWaitLimit, st, 0x5F2);
       }
-      mma_commit(&sm.drain);  // every MMA issued is done before TMEM is released
-      mbar_wait(&sm.drain, 0, kDefaultWaitLimit, st, 0x5F2);
+    } else if (warp == 3) {
+      // ---- scales: fetched kAhead blocks before their use (under the tile loads' traffic a global load takes
+      // longer than a block's MMAs), multiplied, and handed over with the block's sums (d_full counts both) ----
+      const int64_t nblk = (N + 127) / 128;
+      int64_t ftile = first;  // the next block to fetch
+      int fkb = 0;
+      const float *px = xs, *pw = ws;
+      bool in[4];
+      auto aim = [&]() {  // px, pw <- block 0 of tile ftile
+        int64_t m, n;
+        tile_at(ftile, n_mt, n_nt, &m, &n);
+        const int64_t t = m * BM + 128 * rank + lane;
+        px = xs + t;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) in[j] = t + 32 * j < T;
+        // Plain: the tile's columns are weight blocks 2 n and 2 n + 1 (where the
+        // tile ends before the second, its sums are not written). Gated: block n of either matrix.
+        const int64_t wb = GATED ? n : (2 * n + lane < nblk ? 2 * n + lane : nblk - 1);
+        pw = (GATED && lane == 1 ? us : ws) + wb;
+      };
+      auto fetch = [&](int64_t unit) {
+        if (ftile < ntiles) {
+          if (fkb == 0) aim();
+          const int slot = (int)(unit % kRing);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (in[j]) copy4_async(&sm.xs[slot][lane + 32 * j], px + 32 * j);
+          if (lane < 2) copy4_async(&sm.ws[slot][lane], pw);
+          px += T;
+          pw += nblk;
+          if (++fkb == nkb) {
+            fkb = 0;
+            ftile += stride;
+          }
+        }
+        copy_async_commit();
+      };
+      for (int j = 0; j < kAhead; ++j) fetch(j);
+      for (int64_t it = 0; it < units; ++it) {
+        // The slot's last reader was block it - 4; block it - 2 having its sums says that it is done.
+        if (it >= 2 && !mbar_wait_abort(&sm.d_full[it & 1], ((it - 2) >> 1) & 1, limit, st, 0x561, abort_flag)) break;
+        copy_async_wait<kAhead - 1>();
+        __syncwarp();
+        const int slot = (int)(it % kRing);
+        const float w0 = sm.ws[slot][0], w1 = sm.ws[slot][1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = sm.xs[slot][lane + 32 * j];
+          sm.scale[it & 3][0][lane + 32 * j] = x * w0;
+          sm.scale[it & 3][1][lane + 32 * j] = x * w1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.d_full[it & 1]);
+        fetch(it + kAhead);
+      }
+      copy_async_wait<0>();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -239,59 +361,65 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
     const int e = warp - 4, q = warp & 3, half = e >> 2;
     const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
     uint8_t* stage = sm.out[e];
+    const uint32_t d_empty0 = map_to_rank(&sm.d_empty[0], 0);
     uint32_t it = 0;
     bool ok = true;
     // After an abort a warp still walks its tiles, without waits on mbarriers or
     // stores, since the other half of its rows may stand at their barrier.
-    for (int64_t i = blockIdx.x; i < ntiles; i += gridDim.x) {
+    for (int64_t i = first; i < ntiles; i += stride) {
       int64_t m, n;
       tile_at(i, n_mt, n_nt, &m, &n);
-      const int64_t trow = m * 128 + 32 * q, t = trow + lane, tc = t < T ? t : T - 1;
-      const int64_t nblk = (N + 127) / 128;
-      // Weight blocks of this warp's columns. Plain: columns 128 half.. of the
-      // tile are block 2 n + half (clamped when the tile ends before it).
-      // Gated: columns 64 half.. of the gate and of the up tile, both block n.
-      const int64_t wb = GATED ? n : (2 * n + half < nblk ? 2 * n + half : nblk - 1);
-      float2 acc[64];  // plain: 128 columns; gated: 64 gate columns, then the same 64 up columns
+      const int64_t trow = m * BM + 128 * rank + 32 * q, t = trow + lane;
+      float2 acc[2][32];  // plain: 64 + 64 columns; gated: 64 gate columns, the same 64 up columns
 #pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
-      float sx = *(xs + tc), sw = *(ws + wb), su = GATED ? *(us + wb) : 0.0f;
-      for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
-        const float s0 = sx * sw, s1 = GATED ? sx * su : s0;
-        if (kb + 1 < nkb) {
-          sx = *(xs + (int64_t)(kb + 1) * T + tc);
-          sw = *(ws + (int64_t)(kb + 1) * nblk + wb);
-          if (GATED) su = *(us + (int64_t)(kb + 1) * nblk + wb);
-        }
+      for (int c = 0; c < 32; ++c) acc[0][c] = acc[1][c] = make_float2(0.0f, 0.0f);
+      for (int kb = 0; kb < nkb && ok; ++kb) {
         const uint32_t db = it & 1;
         if (!(ok = mbar_wait_abort(&sm.d_full[db], (it >> 1) & 1, limit, st, 0x521, abort_flag))) break;
         tc_fence_after();
-        const uint32_t d = tmem + lane_addr + db * BN;
+        const float sc[2] = {sm.scale[it & 3][GATED ? 0 : half][32 * q + lane],
+                             GATED ? sm.scale[it & 3][1][32 * q + lane] : 0.0f};
+        ++it;
+        // Loads of CW columns, each in flight while the one before is added; the
+        // buffer is released as soon as the last has arrived.
+        constexpr int CW = 16, NC = 128 / CW;
+        const uint32_t d = tmem + lane_addr + db * BN + half * (GATED ? 64 : 128);
+        uint32_t r[2][CW];
+        tmem_ld16(d, r[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          const int col = GATED ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
-          tmem_ld32(d + col, r);
+        for (int c = 0; c < NC; ++c) {
           tmem_ld_wait();
-          const float s = GATED && c >= 2 ? s1 : s0;
-          const float2 s2 = make_float2(s, s);
+          if (c + 1 < NC) {
+            const int col = (c + 1) * CW;
+            tmem_ld16(d + (GATED ? (col / 64) * 128 + col % 64 : col), r[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(d_empty0 + db * 8);
+          }
+          const int h = c * CW / 64;
+          const float v = GATED ? sc[h] : sc[0];
+          const float2 s2 = make_float2(v, v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[16 * c + j] = __ffma2_rn(s2, make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
-                                         acc[16 * c + j]);
+          for (int j = 0; j < CW / 2; ++j) {
+            float2& x = acc[h][(c * CW % 64) / 2 + j];
+            x = __ffma2_rn(s2, make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1])), x);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.d_empty[db]);
       }
       if constexpr (!GATED) {
-        if (ok) write_out<128>(reinterpret_cast<const float(&)[128]>(acc), stage, out, trow, T, n * 256 + 128 * half, N, lane);
+        if (ok) {
+          const int64_t n0 = n * 256 + 128 * half;
+          write_out<64>(reinterpret_cast<const float(&)[64]>(acc[0]), stage, out, trow, T, n0, N, lane);
+          write_out<64>(reinterpret_cast<const float(&)[64]>(acc[1]), stage, out, trow, T, n0 + 64, N, lane);
+        }
       } else {
         float h[64];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          h[2 * c] = f8::activate(acc[c].x, act) * acc[32 + c].x;
-          h[2 * c + 1] = f8::activate(acc[c].y, act) * acc[32 + c].y;
+        switch (act) {
+          case f8::kSilu: f8::gate_row<f8::kSilu>(acc, h); break;
+          case f8::kGelu: f8::gate_row<f8::kGelu>(acc, h); break;
+          case f8::kGeluTanh: f8::gate_row<f8::kGeluTanh>(acc, h); break;
+          default: f8::gate_row<f8::kRelu>(acc, h);
         }
         const int64_t n0 = n * 128 + 64 * half;
         if (out.type != MOBI_E4M3) {
@@ -327,12 +455,15 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
     }
   }
 
+  // Neither CTA leaves, or releases its TMEM, while the other may still use it.
   tc_fence_before();
   __syncthreads();
+  cluster_arrive();
+  cluster_wait();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -382,8 +513,7 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int32_t* abort_flag = &sm.abort_flag;
-  uint32_t rank;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t rank = cluster_rank();
   const int64_t n0 = (int64_t)(blockIdx.x / csize) * 128, t0 = (int64_t)blockIdx.y * BN;
   const int kb0 = (int)((int64_t)nkb * rank / csize), kb1 = (int)((int64_t)nkb * (rank + 1) / csize);
   const int64_t nblk = (N + 127) / 128, wb = n0 / 128;
@@ -431,21 +561,32 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     if (lane == 0) {
       // ---- MMA issuer ----
       constexpr uint32_t idesc = idesc_e4m3(128, BN);
-      uint32_t it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t s = it % CF::ST, db = it % CF::DST;
-        if (!mbar_wait_abort(&sm.full[s], (it / CF::ST) & 1, limit, st, 0x541, abort_flag)) break;
-        if (!mbar_wait_abort(&sm.d_empty[db], ((it / CF::DST) & 1) ^ 1, limit, st, 0x542, abort_flag)) break;
+      const uint64_t w0 = desc_sw128(smem_addr(&sm.w[0][0])), x0 = desc_sw128(smem_addr(&sm.x[0][0]));
+      uint32_t s = 0, ph = 0, db = 0, dph = 1;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_abort(&sm.full[s], ph, limit, st, 0x541, abort_flag)) break;
+        if (!mbar_wait_abort(&sm.d_empty[db], dph, limit, st, 0x542, abort_flag)) break;
         tc_fence_after();
-        const uint32_t w = smem_addr(&sm.w[s][0]), x = smem_addr(&sm.x[s][0]);
+        const uint64_t w = w0 + s * (CF::kWBytes / 16), x = x0 + s * (CF::kXBytes / 16);
 #pragma unroll
-        for (int mt = 0; mt < CF::MATS; ++mt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss_f8(tmem + db * CF::COLS + mt * BN, desc_sw128(w + mt * f8::kTileBytes + 32 * k),
-                      desc_sw128(x + 32 * k), idesc, k > 0);
+        for (int mt = 0; mt < CF::MATS; ++mt) {
+          const uint32_t d = tmem + db * CF::COLS + mt * BN;
+          const uint64_t wm = w + mt * (f8::kTileBytes / 16);
+          mma_ss_f8<false>(d, wm, x, idesc);
+          mma_ss_f8<true>(d, wm + 2, x + 2, idesc);
+          mma_ss_f8<true>(d, wm + 4, x + 4, idesc);
+          mma_ss_f8<true>(d, wm + 6, x + 6, idesc);
+        }
         mma_commit(&sm.empty[s]);
         mma_commit(&sm.d_full[db]);
+        if (++s == CF::ST) {
+          s = 0;
+          ph ^= 1;
+        }
+        if (++db == CF::DST) {
+          db = 0;
+          dph ^= 1;
+        }
       }
       mma_commit(&sm.drain);
       mbar_wait(&sm.drain, 0, kDefaultWaitLimit, st, 0x5F4);
@@ -523,8 +664,8 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     }
   }
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 
   if (warp < 8) {
     const int row = threadIdx.x & 127;
@@ -585,8 +726,8 @@ struct Fp8Plan {
 static Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   Fp8Plan p;
   const int64_t nkb = (K + 127) / 128, nt = (N + 127) / 128;
-  const int64_t wide_tiles = ((T + 127) / 128) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
-  p.wide = T > 128 && 2 * wide_tiles >= sms;
+  const int64_t wide_tiles = ((T + 255) / 256) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  p.wide = T > 128 && 4 * wide_tiles >= sms;
   p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || gated ? 64 : 128));
   const int64_t tiles = nt * ((T + p.bn - 1) / p.bn);
   const int64_t room = (p.bn <= 32 ? 2 : 1) * (int64_t)sms;
@@ -617,7 +758,7 @@ static cudaError_t launch_fp8(const Fp8Job& j, cudaStream_t stream) {
   const int sms = num_sms();
   const Fp8Plan p = fp8_plan(j.T, j.N, j.K, GATED, sms);
   CUtensorMap mx, mw, mu = {};
-  const uint32_t rows_x = p.wide ? 128 : (uint32_t)p.bn, rows_w = p.wide && !GATED ? 256 : 128;
+  const uint32_t rows_x = p.wide ? 128 : (uint32_t)p.bn, rows_w = 128;
   if (!make_tmap_u8(&mx, j.X, (uint64_t)j.K, (uint64_t)j.T, (uint64_t)j.ldx, rows_x) ||
       !make_tmap_u8(&mw, j.W, (uint64_t)j.K, (uint64_t)j.N, (uint64_t)j.ldw, rows_w) ||
       (GATED && !make_tmap_u8(&mu, j.U, (uint64_t)j.K, (uint64_t)j.N, (uint64_t)j.ldu, rows_w)))
@@ -636,8 +777,9 @@ static cudaError_t launch_fp8(const Fp8Job& j, cudaStream_t stream) {
   static_assert(smem <= 232448, "shared memory");
   e = set_smem((const void*)fp8_wide_kernel<GATED>, smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((j.T + 127) / 128) * ((j.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-  e = launch_dependent(fp8_wide_kernel<GATED>, dim3((unsigned)(tiles < sms ? tiles : sms)), f8w::kThreads, smem, 1,
+  const int64_t tiles = ((j.T + f8w::BM - 1) / f8w::BM) * ((j.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  e = launch_dependent(fp8_wide_kernel<GATED>, dim3((unsigned)(2 * pairs)), f8w::kThreads, smem, 2,
                        stream, mx, mw, mu, j.xs, j.ws, j.us, j.T, j.N, (int)((j.K + 127) / 128), j.act, j.out, st,
                        wait_limit());
   return note_error("fp8 wide launch", e);

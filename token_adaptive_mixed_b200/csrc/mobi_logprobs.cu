@@ -277,8 +277,7 @@ __device__ void top_keys(Smem& sm, const Part<E>& p, int k) {
 // An 8-byte or 4-byte word of CTA `rank`'s shared memory (the same variable there).
 template <typename V>
 __device__ __forceinline__ V remote(const V* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  const uint32_t a = map_to_rank(p, rank);
   V v;
   if constexpr (sizeof(V) == 8)
     asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
@@ -354,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   if (csize > 1) {
     __syncthreads();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
     if (rank == 0) {
       if (tid == 0) {
         Stat all = sm.total;
@@ -379,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     // CTA 0 has read the others' shared memory before they leave.
     __syncthreads();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
     if (rank != 0) return;
   }
   __syncthreads();
