@@ -580,7 +580,7 @@ enum { MOBI_F32 = 0, MOBI_BF16 = 1, MOBI_F16 = 2, MOBI_E4M3 = 3 };
  * A block is 1 x 128 (block_rows = 1: activations, one token's values of one
  * group of 128 along K) or 128 x 128 (block_rows = 128: weights). With
  * a = max |x| over the block,
- *   s = max(a / 448, 2^-126)          (fp32)
+ *   s = max(a * c, 2^-126)            (fp32, c = 1/448 rounded to fp32)
  *   q = e4m3(x * (1 / s))             (both in fp32; to nearest even, saturating)
  * so q * s stands for x. A block that holds a NaN or an infinity gets a NaN or
  * infinite scale and NaN codes in its place: whatever it enters becomes NaN.

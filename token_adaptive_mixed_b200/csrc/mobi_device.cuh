@@ -113,6 +113,12 @@ __device__ __forceinline__ bool mbar_wait_abort(uint64_t* bar, uint32_t parity, 
   return false;
 }
 
+// The same for a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool mbar_wait_abort_warp(uint64_t* bar, uint32_t parity, uint64_t limit, DeviceStatus* st,
+                                                     uint32_t where, volatile int32_t* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait_abort(bar, parity, limit, st, where, abort_flag));
+}
+
 // ---- CTA pairs (cta_group::2: two CTAs of a cluster share one MMA) -------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -353,16 +359,23 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
 // ---- 8-bit blocks ---------------------------------------------------------------
 //
 // A block of 128 values is held as e4m3 values q with one fp32 scale s: with
-// a = max |x| over the block, s = max(a / 448, 2^-126) and q = e4m3(x * (1 / s)),
-// rounded to nearest even and saturating. `amax_bits` is a's bit pattern: the
+// a = max |x| over the block and c = fp32(1/448), s = max(a * c, 2^-126) and
+// q = e4m3(x * (1 / s)), rounded to nearest even and saturating. `amax_bits` is a's bit pattern: the
 // patterns of |x| order as integers with NaN above infinity, so an integer
 // maximum carries a NaN on, which fmaxf would drop. A NaN or an infinity in a
 // block gives it a NaN or infinite scale, and so NaN outputs wherever it enters.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-  const float s = __uint_as_float(amax_bits) / 448.0f;
+  const float s = __uint_as_float(amax_bits) * (1.0f / 448.0f);
   return s < 1.17549435e-38f ? 1.17549435e-38f : s;
+}
+
+// max(a, |x|), NaN if either is: the same order as abs_bits in one instruction.
+__device__ __forceinline__ float max_abs(float a, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(x)));
+  return r;
 }
 
 // Two values as e4m3, `lo` in the low byte.

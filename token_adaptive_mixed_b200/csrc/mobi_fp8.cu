@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       // Issuing waits for room in the tensor pipe's short queue, a barrier check
       // takes about 100 clocks even where it is ready, and a commit half of that:
       // one thread alone left the pipe idle for half of the time. Each thread
-      // tests the next block's stage while it issues this one.
+      // tests the next block's stage while it issues this one: that asks for block
+      // u + 2's phase of its stage, which block u - 3 used before; block u's buffer
+      // being free says that u - 2 and all before it have gone through.
       if (lane == 0 && rank == 0) {
         constexpr uint32_t idesc = idesc_e4m3(BM, BN);
         const uint64_t a0 = desc_sw128(smem_addr(&sm.a[0][0])), b0 = desc_sw128(smem_addr(&sm.b[0][0]));
@@ -338,7 +340,8 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       for (int j = 0; j < kAhead; ++j) fetch(j);
       for (int64_t it = 0; it < units; ++it) {
         // The slot's last reader was block it - 4; block it - 2 having its sums says that it is done.
-        if (it >= 2 && !mbar_wait_abort(&sm.d_full[it & 1], ((it - 2) >> 1) & 1, limit, st, 0x561, abort_flag)) break;
+        if (it >= 2 && !mbar_wait_abort_warp(&sm.d_full[it & 1], ((it - 2) >> 1) & 1, limit, st, 0x561, abort_flag))
+          break;
         copy_async_wait<kAhead - 1>();
         __syncwarp();
         const int slot = (int)(it % kRing);
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       for (int c = 0; c < 32; ++c) acc[0][c] = acc[1][c] = make_float2(0.0f, 0.0f);
       for (int kb = 0; kb < nkb && ok; ++kb) {
         const uint32_t db = it & 1;
-        if (!(ok = mbar_wait_abort(&sm.d_full[db], (it >> 1) & 1, limit, st, 0x521, abort_flag))) break;
+        if (!(ok = mbar_wait_abort_warp(&sm.d_full[db], (it >> 1) & 1, limit, st, 0x521, abort_flag))) break;
         tc_fence_after();
         const float sc[2] = {sm.scale[it & 3][GATED ? 0 : half][32 * q + lane],
                              GATED ? sm.scale[it & 3][1][32 * q + lane] : 0.0f};
@@ -470,30 +473,41 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
 // ---- narrow: weight rows on lanes, K split over a cluster ------------------------------
 
 namespace f8n {
-constexpr int kThreads = 10 * 32;  // 0-7 epilogue, 8 producer, 9 MMA
+constexpr int kThreads = 12 * 32;       // 0-7 epilogue, 8 producer, 9 and 10 MMA, 11 scales
+constexpr int kRing = 8, kAhead = 6;    // fetched scales: slots, and blocks between the fetch and the use
 
 template <bool GATED, int BN>
 struct Cfg {
   static constexpr int MATS = GATED ? 2 : 1;
   static constexpr int COLS = MATS * BN;                     // accumulator columns of one block's sums
   static constexpr int HC = COLS / 2;                        // of which an epilogue warp takes half
-  static constexpr int DST = COLS <= 32 ? 4 : 2;             // accumulator buffers in TMEM
-  static constexpr int TMEM = DST * COLS < 32 ? 32 : DST * COLS;
+  static constexpr int DST = 4;                              // accumulator buffers in TMEM (block & 3)
+  static constexpr int TMEM = DST * COLS;
   static constexpr uint32_t kWBytes = MATS * f8::kTileBytes, kXBytes = BN * f8::BK;
   static constexpr uint32_t kStage = kWBytes + kXBytes;
-  // Stages: as many bytes in flight as one (BN >= 64) or two CTAs of an SM can hold.
-  static constexpr int ST = GATED ? (BN == 64 ? 3 : 2) : (BN == 16 ? 5 : (BN == 64 ? 6 : 4));
-  static constexpr int kPerSm = BN <= 32 ? 2 : 1;            // CTAs that share an SM
-  static_assert(HC >= 8 && HC <= 64 && TMEM <= 512 && (TMEM & (TMEM - 1)) == 0, "tile");
+  static constexpr int kPerSm = COLS <= 64 ? 2 : 1;          // CTAs that share an SM
+  // Stages: about 100 KB (two CTAs) or 190 KB in flight, which covers the memory's latency at its bandwidth.
+  static constexpr int ST = GATED ? (BN == 64 ? 5 : 3) : (BN == 16 ? 6 : (BN == 32 ? 5 : (BN == 64 ? 4 : 6)));
+  static_assert(HC >= 8 && HC <= 64 && TMEM * kPerSm <= 512 && (TMEM & (TMEM - 1)) == 0, "tile");
+  static constexpr int MT = ST >= 4 ? 2 : 1;                 // MMA threads (see there)
+  static constexpr int kRed = (COLS + 8 * MATS) * 128;       // the cluster's sums (tokens rounded up for each owner)
+  static_assert(kRed * 4 <= ST * kStage, "the cluster's sums take the stages' place");
 };
 
 template <bool GATED, int BN>
 struct Smem {
   using C = Cfg<GATED, BN>;
-  uint8_t w[C::ST][C::kWBytes];          // 1024-byte aligned (offset 0)
-  uint8_t x[C::ST][C::kXBytes];
-  float red[C::COLS * 128];              // [source rank][owned column][row]: the cluster's sums of the owned tokens
-  float scale[f8::kEpiWarps][2][64];     // per warp: block scales of its columns, double-buffered
+  union {
+    struct {
+      uint8_t w[C::ST][C::kWBytes];      // 1024-byte aligned (offset 0)
+      uint8_t x[C::ST][C::kXBytes];
+    };
+    // After the last block: [source rank][owned column][row], the cluster's sums of the owned tokens.
+    float red[C::kRed];
+  };
+  float xs[kRing][BN];                   // fetched scales of the tile's tokens and weight blocks
+  float ws[kRing][2];
+  float scale[4][C::COLS];               // their products, by accumulator column
   uint32_t colmax[2][2][4];
   uint64_t full[C::ST], empty[C::ST], d_full[C::DST], d_empty[C::DST], drain;
   uint32_t tmem_base;
@@ -504,10 +518,12 @@ struct Smem {
 template <bool GATED, int BN>
 __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_u, const float* xs,
-                      const float* ws, const float* us, int64_t T, int64_t N, int nkb,
-                      int csize, int act, f8::Out out, DeviceStatus* st, uint64_t limit) {
+                      const __grid_constant__ CUtensorMap tm_u, const float* xs, const float* ws, const float* us,
+                      int64_t T, int64_t N, int nkb, int csize, int act, f8::Out out, DeviceStatus* st,
+                      uint64_t limit) {
   using CF = f8n::Cfg<GATED, BN>;
+  using f8n::kAhead;
+  using f8n::kRing;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   f8n::Smem<GATED, BN>& sm = *reinterpret_cast<f8n::Smem<GATED, BN>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -519,9 +535,12 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
   const int64_t nblk = (N + 127) / 128, wb = n0 / 128;
 
   if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_x);
+    if (GATED) prefetch_tmap(&tm_u);
     for (int i = 0; i < CF::ST; ++i) { mbar_init(&sm.full[i], 1); mbar_init(&sm.empty[i], 1); }
-    for (int i = 0; i < CF::DST; ++i) { mbar_init(&sm.d_full[i], 1); mbar_init(&sm.d_empty[i], f8::kEpiWarps); }
-    mbar_init(&sm.drain, 1);
+    for (int i = 0; i < CF::DST; ++i) { mbar_init(&sm.d_full[i], 2); mbar_init(&sm.d_empty[i], f8::kEpiWarps); }
+    mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
@@ -530,12 +549,9 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  // Every CTA of the cluster runs before its shared memory is written (waited for below).
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  constexpr int NPER = CF::HC < 32 ? 1 : CF::HC / 32;  // scales a lane fetches
   float2 acc[CF::HC / 2];
 #pragma unroll
   for (int c = 0; c < CF::HC / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
@@ -545,88 +561,129 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
   if (warp == 8) {
     if (lane == 0) {
       // ---- TMA producer ----
-      uint32_t it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t s = it % CF::ST;
-        if (!mbar_wait_abort(&sm.empty[s], ((it / CF::ST) & 1) ^ 1, limit, st, 0x531, abort_flag)) break;
+      uint32_t s = 0, ph = 1;
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
+        if (!mbar_wait_abort(&sm.empty[s], ph, limit, st, 0x531, abort_flag)) break;
         mbar_arrive_expect_tx(&sm.full[s], CF::kStage);
         tma_load_2d(&sm.w[s][0], &tm_w, kb * f8::BK, (int)n0, &sm.full[s]);
         if (GATED) tma_load_2d(&sm.w[s][f8::kTileBytes], &tm_u, kb * f8::BK, (int)n0, &sm.full[s]);
         tma_load_2d(&sm.x[s][0], &tm_x, kb * f8::BK, (int)t0, &sm.full[s]);
-      }
-      for (uint32_t j = (it > CF::ST ? it - CF::ST : 0); j < it; ++j)
-        mbar_wait(&sm.full[j % CF::ST], (j / CF::ST) & 1, kDefaultWaitLimit, st, 0x5F3);
-    }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      // ---- MMA issuer ----
-      constexpr uint32_t idesc = idesc_e4m3(128, BN);
-      const uint64_t w0 = desc_sw128(smem_addr(&sm.w[0][0])), x0 = desc_sw128(smem_addr(&sm.x[0][0]));
-      uint32_t s = 0, ph = 0, db = 0, dph = 1;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_abort(&sm.full[s], ph, limit, st, 0x541, abort_flag)) break;
-        if (!mbar_wait_abort(&sm.d_empty[db], dph, limit, st, 0x542, abort_flag)) break;
-        tc_fence_after();
-        const uint64_t w = w0 + s * (CF::kWBytes / 16), x = x0 + s * (CF::kXBytes / 16);
-#pragma unroll
-        for (int mt = 0; mt < CF::MATS; ++mt) {
-          const uint32_t d = tmem + db * CF::COLS + mt * BN;
-          const uint64_t wm = w + mt * (f8::kTileBytes / 16);
-          mma_ss_f8<false>(d, wm, x, idesc);
-          mma_ss_f8<true>(d, wm + 2, x + 2, idesc);
-          mma_ss_f8<true>(d, wm + 4, x + 4, idesc);
-          mma_ss_f8<true>(d, wm + 6, x + 6, idesc);
-        }
-        mma_commit(&sm.empty[s]);
-        mma_commit(&sm.d_full[db]);
         if (++s == CF::ST) {
           s = 0;
           ph ^= 1;
         }
-        if (++db == CF::DST) {
-          db = 0;
+      }
+      for (int j = 0; j < CF::ST && j < kb - kb0; ++j) {  // every copy lands before its stage is used again
+        s = s == 0 ? CF::ST - 1 : s - 1;
+        if (s == CF::ST - 1) ph ^= 1;
+        mbar_wait(&sm.full[s], ph ^ 1, kDefaultWaitLimit, st, 0x5F3);
+      }
+    }
+  } else if (warp == 9 || warp == 10) {
+    if (lane == 0) {
+      // ---- MMA issuers: with MT = 2, warp 9 takes the even blocks and warp 10 the odd ones (a block's
+      // instructions take one thread longer than its MMAs run) ----
+      // A parity wait tells a phase from the one before it only, so a thread may
+      // wait for block u's stage once block u - ST has gone through it. With two
+      // threads that follows from the buffer: it is free when block u - 4 has been
+      // added, and blocks are added in order, so ST >= 4 is needed there.
+      constexpr int MT = CF::MT;
+      constexpr uint32_t idesc = idesc_e4m3(128, BN);
+      const uint64_t w0 = desc_sw128(smem_addr(&sm.w[0][0])), x0 = desc_sw128(smem_addr(&sm.x[0][0]));
+      const int first = warp - 9;
+      uint32_t s = (uint32_t)first, ph = 0, db = s, dph = 1;
+      for (int kb = first < MT ? kb0 + first : kb1; kb < kb1; kb += MT) {
+        if (!mbar_wait_abort(&sm.d_empty[db], dph, limit, st, 0x542, abort_flag)) break;
+        if (!mbar_wait_abort(&sm.full[s], ph, limit, st, 0x541, abort_flag)) break;
+        tc_fence_after();
+        const uint64_t w = w0 + s * (CF::kWBytes / 16), x = x0 + s * (CF::kXBytes / 16);
+        const uint32_t d = tmem + db * CF::COLS, s0 = s, db0 = db;
+        s += MT;
+        if (s >= CF::ST) {
+          s -= CF::ST;
+          ph ^= 1;
+        }
+        db += MT;
+        if (db >= 4) {
+          db -= 4;
           dph ^= 1;
         }
+#pragma unroll
+        for (int mt = 0; mt < CF::MATS; ++mt) {
+          const uint64_t wm = w + mt * (f8::kTileBytes / 16);
+          mma_ss_f8<false>(d + mt * BN, wm, x, idesc);
+          mma_ss_f8<true>(d + mt * BN, wm + 2, x + 2, idesc);
+          mma_ss_f8<true>(d + mt * BN, wm + 4, x + 4, idesc);
+          mma_ss_f8<true>(d + mt * BN, wm + 6, x + 6, idesc);
+        }
+        mma_commit(&sm.d_full[db0]);
+        mma_commit(&sm.empty[s0]);
       }
       mma_commit(&sm.drain);
       mbar_wait(&sm.drain, 0, kDefaultWaitLimit, st, 0x5F4);
     }
-  } else {
-    // ---- epilogue: promotion; a lane fetches some of the warp's column scales a block ahead ----
-    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
-    const float* wsc = mat ? us : ws;
-    int64_t tok[NPER];
+  } else if (warp == 11) {
+    // ---- scales: fetched kAhead blocks ahead, multiplied, handed over with the block's sums ----
+    constexpr int NX = (BN + 31) / 32;
+    const float* px = xs + (int64_t)kb0 * T + t0 + lane;
+    const float* pw = (GATED && lane == 1 ? us : ws) + (int64_t)kb0 * nblk + wb;
+    bool in[NX];
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const int64_t t = t0 + j0 + lane % CF::HC + 32 * i;
-      tok[i] = t < T ? t : T - 1;
-    }
-    float nx[NPER], nw;
-    nw = *(wsc + (int64_t)kb0 * nblk + wb);
+    for (int j = 0; j < NX; ++j) in[j] = lane + 32 * j < BN && t0 + lane + 32 * j < T;
+    auto fetch = [&](int i) {  // block kb0 + i
+      if (kb0 + i < kb1) {
+        const int slot = i % kRing;
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) nx[i] = *(xs + (int64_t)kb0 * T + tok[i]);
-    uint32_t it = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      float* sc = sm.scale[warp][it & 1];
+        for (int j = 0; j < NX; ++j)
+          if (in[j]) copy4_async(&sm.xs[slot][lane + 32 * j], px + 32 * j);
+        if (lane < CF::MATS) copy4_async(&sm.ws[slot][lane], pw);
+        px += T;
+        pw += nblk;
+      }
+      copy_async_commit();
+    };
+    for (int i = 0; i < kAhead; ++i) fetch(i);
+    bool have = true;
+    for (int i = 0; kb0 + i < kb1; ++i) {
+      // The slot's last readers took block i - 4, whose buffer block i's MMAs wait for as well.
+      if (!__all_sync(0xffffffffu, have) &&
+          !mbar_wait_abort_warp(&sm.d_empty[i & 3], ((i >> 2) - 1) & 1, limit, st, 0x562, abort_flag))
+        break;
+      copy_async_wait<kAhead - 1>();
+      __syncwarp();
+      const int slot = i % kRing;
+      const float w0 = sm.ws[slot][0], w1 = sm.ws[slot][CF::MATS - 1];
 #pragma unroll
-      for (int i = 0; i < NPER; ++i)
-        if (CF::HC >= 32 || lane < CF::HC) sc[lane + 32 * i] = nx[i] * nw;
-      if (kb + 1 < kb1) {
-        nw = *(wsc + (int64_t)(kb + 1) * nblk + wb);
-#pragma unroll
-        for (int i = 0; i < NPER; ++i) nx[i] = *(xs + (int64_t)(kb + 1) * T + tok[i]);
+      for (int j = 0; j < NX; ++j) {
+        const int c = lane + 32 * j;
+        if (c < BN) {
+          const float x = in[j] ? sm.xs[slot][c] : 0.0f;
+          sm.scale[i & 3][c] = x * w0;
+          if (GATED) sm.scale[i & 3][BN + c] = x * w1;
+        }
       }
       __syncwarp();
-      const uint32_t db = it % CF::DST;
-      if (!mbar_wait_abort(&sm.d_full[db], (it / CF::DST) & 1, limit, st, 0x551, abort_flag)) break;
+      if (lane == 0) mbar_arrive(&sm.d_full[i & 3]);
+      have = i + 1 < 4 || mbar_test_wait(&sm.d_empty[(i + 1) & 3], (((i + 1) >> 2) - 1) & 1);
+      fetch(i + kAhead);
+    }
+    copy_async_wait<0>();
+  } else {
+    // ---- epilogue: promotion by the column's scale ----
+    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
+    for (int i = 0; kb0 + i < kb1; ++i) {
+      const uint32_t db = i & 3;
+      if (!mbar_wait_abort_warp(&sm.d_full[db], (i >> 2) & 1, limit, st, 0x551, abort_flag)) break;
       tc_fence_after();
+      const float* sc = &sm.scale[db][half * CF::HC];
       const uint32_t d = tmem + lane_addr + db * CF::COLS + half * CF::HC;
-      constexpr int LC = CF::HC < 32 ? CF::HC : 32;  // columns per TMEM load
+      constexpr int LC = CF::HC < 16 ? CF::HC : (CF::kPerSm == 2 ? 16 : 32);  // columns per TMEM load
 #pragma unroll
       for (int c = 0; c < CF::HC / LC; ++c) {
         uint32_t r[LC];
         if constexpr (LC == 8) tmem_ld8(d, r);
-        if constexpr (LC == 16) tmem_ld16(d, r);
+        if constexpr (LC == 16) tmem_ld16(d + 16 * c, r);
         if constexpr (LC == 32) tmem_ld32(d + 32 * c, r);
         tmem_ld_wait();
 #pragma unroll
@@ -645,22 +702,27 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     }
   }
 
-  // The cluster's sums: CTA r owns tokens [r BN / csize, (r + 1) BN / csize) of
-  // the tile; every CTA writes its sums of them into r's shared memory, and r
-  // adds them in rank order (the result does not depend on who finishes first).
+  // The cluster's sums: CTA r owns the tokens [r tpc, (r + 1) tpc) of the tile;
+  // every CTA writes its sums of them into r's shared memory, and r adds them in
+  // rank order (the result does not depend on who finishes first). The sums take
+  // the stages' place, so every CTA is through with its blocks first.
   __syncwarp();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  const int tpc = BN / csize;
+  cluster_arrive();
+  cluster_wait();
+  const int tpc = (BN + csize - 1) / csize;
   if (warp < 8) {
-    const uint32_t red = smem_addr(&sm.red[0]);
+    const uint32_t red = smem_addr(&sm.red[0]) + (uint32_t)(((int)rank * CF::MATS + mat) * tpc * 128 + 32 * q + lane) * 4;
+    int owner = j0 / tpc, slot = j0 % tpc;
 #pragma unroll
     for (int c = 0; c < CF::HC; ++c) {
-      const int j = j0 + c, owner = j / tpc, slot = mat * tpc + j % tpc;
-      const uint32_t local = red + (uint32_t)((((int)rank * CF::MATS * tpc + slot) * 128 + 32 * q + lane) * 4);
       uint32_t remote;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(owner));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(red + slot * 512), "r"(owner));
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"((c & 1) ? acc[c >> 1].y : acc[c >> 1].x)
                    : "memory");
+      if (++slot == tpc) {
+        slot = 0;
+        ++owner;
+      }
     }
   }
   __syncwarp();
@@ -673,7 +735,7 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     const int per = CF::MATS * tpc * 128;
     for (int tl = half; tl < tpc; tl += 2) {  // tokens of this CTA, alternating between the two groups of 128 threads
       const int64_t t = t0 + (int64_t)rank * tpc + tl;
-      if (t >= T) break;
+      if (t >= T || (int)rank * tpc + tl >= BN) break;
       float v = 0.0f, u = 0.0f;
       for (int c = 0; c < csize; ++c) {
         v += sm.red[c * per + tl * 128 + row];
@@ -723,16 +785,29 @@ struct Fp8Plan {
   int bn, csize;
 };
 
+// Narrow: the token tile is the batch rounded up, to 128 (gated 64) at most,
+// and K is cut over as many CTAs as fit at once, two blocks each at least.
+// From 33 tokens on both kernels' times are estimated from their waves and
+// blocks: measured at K = 4096 (N = 4096 and 11008, T = 64 .. 1024), the wide
+// kernel takes 0.52 us a block and wave (fewer SMs, but a quarter of the time per
+// output) and the narrow one 0.85 us a block of its CTA's share. T = 333,
+// N = 4099: 20 us against 32; T = 64, N = 11008: 22 us against 16.
 static Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   Fp8Plan p;
   const int64_t nkb = (K + 127) / 128, nt = (N + 127) / 128;
-  const int64_t wide_tiles = ((T + 255) / 256) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
-  p.wide = T > 128 && 4 * wide_tiles >= sms;
   p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || gated ? 64 : 128));
   const int64_t tiles = nt * ((T + p.bn - 1) / p.bn);
-  const int64_t room = (p.bn <= 32 ? 2 : 1) * (int64_t)sms;
-  p.csize = 1;
-  while (p.csize < 8 && tiles * p.csize * 2 <= room && nkb >= 2 * p.csize) p.csize *= 2;
+  const int64_t room = (p.bn * (gated ? 2 : 1) <= 64 ? 2 : 1) * (int64_t)sms;
+  int64_t c = room / tiles;
+  if (c > nkb / 2) c = nkb / 2;
+  p.csize = (int)(c < 1 ? 1 : (c > 8 ? 8 : c));
+  p.wide = false;
+  if (T > 32) {
+    const int64_t wt = ((T + f8w::BM - 1) / f8w::BM) * (gated ? nt : (nt + 1) / 2);
+    const int64_t wide = 450 + (wt + sms / 2 - 1) / (sms / 2) * nkb * 52;
+    const int64_t narrow = 600 + (tiles * p.csize + room - 1) / room * ((nkb + p.csize - 1) / p.csize) * 85;
+    p.wide = wide < narrow;
+  }
   return p;
 }
 

@@ -3,11 +3,13 @@
 //   r = x + scale * gate * z
 //   n = norm(r) * weight + bias, also as e4m3 blocks of 128 (mobi_device.cuh, "8-bit blocks")
 //
-// Memory-bound: block and x are read once and r and n written once; a row
-// lives in registers between (eight consecutive values per thread and chunk,
-// NCH chunks), so both norms' statistics are exact two-pass sums in fp32 (mean
-// first, then squares of the differences) at no extra traffic. Sixteen lanes
-// hold the 128 values of an e4m3 block.
+// Memory-bound: block and x are read once and r and n written once. A row lives
+// in registers between (eight consecutive values per thread and octet), so both
+// norms' statistics are exact two-pass sums in fp32 (mean first, then squares of
+// the differences) at no extra traffic. Sixteen lanes hold the 128 values of an
+// e4m3 block. A CTA walks over rows: the next row's loads are in flight while
+// this one is summed; the weights stay in L1 for all of them (held in registers
+// they cost the second CTA of an SM).
 #include <cmath>
 #include <cstdint>
 
@@ -24,15 +26,17 @@ struct Params {
   int tpr;                     // threads of a row
 };
 
-// Eight raw elements: `a` holds 16-bit types, `a` and `b` fp32.
+// Eight raw elements of ES bytes.
+template <int ES>
 struct Raw8 {
-  uint4 a, b;
+  uint32_t w[2 * ES];
 };
 
-// Element `i` of a raw octet of `dtype` as fp32.
-__device__ __forceinline__ void widen8(const Raw8& r, int dtype, float (&v)[8]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-  if (dtype == MOBI_F32) {
+// An octet as fp32; `dtype` tells the two 16-bit types apart.
+template <int ES>
+__device__ __forceinline__ void widen8(const Raw8<ES>& r, int dtype, float (&v)[8]) {
+  const uint32_t* w = r.w;
+  if constexpr (ES == 4) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   } else if (dtype == MOBI_BF16) {
@@ -50,28 +54,39 @@ __device__ __forceinline__ void widen8(const Raw8& r, int dtype, float (&v)[8]) 
   }
 }
 
-// Elements d .. d+7 of a row at `base` + off elements (stride 1), zeros from D on.
-__device__ __forceinline__ Raw8 load8(const void* base, int dtype, int64_t off, int d, int D, int vec) {
-  Raw8 r;
-  r.a = r.b = make_uint4(0, 0, 0, 0);
+// Elements d .. d+7 of a row at `base` + off elements, zeros from D on.
+template <int ES>
+__device__ __forceinline__ Raw8<ES> load8(const void* base, int64_t off, int d, int D, int vec) {
+  Raw8<ES> r;
+#pragma unroll
+  for (int i = 0; i < 2 * ES; ++i) r.w[i] = 0;
   if (d >= D) return r;
-  const int es = dtype == MOBI_F32 ? 4 : 2;
-  const uint8_t* p = static_cast<const uint8_t*>(base) + (off + d) * es;
+  const uint8_t* p = static_cast<const uint8_t*>(base) + (off + d) * ES;
   if (vec && d + 8 <= D) {
-    r.a = *reinterpret_cast<const uint4*>(p);
-    if (es == 4) r.b = *reinterpret_cast<const uint4*>(p + 16);
+#pragma unroll
+    for (int i = 0; i < ES / 2; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
+    }
     return r;
   }
-  uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (d + i < D) {
-      if (es == 4) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-      else w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+      if constexpr (ES == 4) r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      else r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
     }
-  r.a = make_uint4(w[0], w[1], w[2], w[3]);
-  r.b = make_uint4(w[4], w[5], w[6], w[7]);
   return r;
+}
+
+// The same of a type known at run time only, as fp32.
+__device__ __forceinline__ void load8_f32(const void* base, int dtype, int64_t off, int d, int D, int vec,
+                                          float (&v)[8]) {
+  if (dtype == MOBI_F32) widen8<4>(load8<4>(base, off, d, D, vec), dtype, v);
+  else widen8<2>(load8<2>(base, off, d, D, vec), dtype, v);
 }
 
 __device__ __forceinline__ void store8(void* base, int dtype, int64_t off, int d, int D, int vec, const float (&v)[8]) {
@@ -124,150 +139,493 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[32], int
   return v;
 }
 
-// v <- kind(v) * w + b over a row.
+// 1 / sqrt(m): the approximate reciprocal root with one Newton step (fp32 to the
+// last place or two). Zero and infinity keep the first estimate, infinity and
+// 0, which the step would turn into a NaN.
+__device__ __forceinline__ float root(float m) {
+  const float y = rsqrtf(m);
+  return m == 0.0f || y == 0.0f ? y : y * fmaf(-0.5f * m * y, y, 1.5f);
+}
+
+// v <- kind(v) * w + b over a row (zeros past D stay out of the sums).
 template <int NCH>
 __device__ __forceinline__ void norm_row(float (&v)[NCH][8], int kind, float eps, const void* weight, const void* bias,
-                                         const Params& p, int l, float (*red)[32], int slot) {
+                                         const Params& p, int l, float inv, float (*red)[32], int slot) {
   const int D = (int)p.a.D, tpr = p.tpr;
-  const float inv = 1.0f / (float)D;
   float mean = 0.0f, s = 0.0f;
   if (kind == MOBI_NORM_LAYER) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[c][i];  // zeros past D
+      for (int i = 0; i < 8; ++i) s += v[c][i];
     mean = row_sum(s, tpr, red, slot) * inv;
     s = 0.0f;
   }
   float rstd = 1.0f;
   if (kind != MOBI_NORM_NONE) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < NCH; ++c) {
+      const int d = (c * tpr + l) * 8;
+      if (d + 8 <= D) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = (c * tpr + l) * 8 + i < D ? v[c][i] - mean : 0.0f;
-        s = fmaf(e, e, s);
+        for (int i = 0; i < 8; ++i) s = fmaf(v[c][i] - mean, v[c][i] - mean, s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (d + i < D) s = fmaf(v[c][i] - mean, v[c][i] - mean, s);
       }
-    rstd = 1.0f / sqrtf(row_sum(s, tpr, red, slot + 1) * inv + eps);
+    }
+    rstd = root(row_sum(s, tpr, red, slot + 1) * inv + eps);
   }
   const float one = p.a.unit_offset ? 1.0f : 0.0f;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int d = (c * tpr + l) * 8;
-    float w[8], b[8];
-    if (weight) widen8(load8(weight, p.a.weight_dtype, 0, d, D, p.vw), p.a.weight_dtype, w);
-    if (bias) widen8(load8(bias, p.a.weight_dtype, 0, d, D, p.vw), p.a.weight_dtype, b);
+    float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float e = (v[c][i] - mean) * rstd;
-      if (weight) e *= w[i] + one;
-      if (bias) e += b[i];
-      v[c][i] = e;
+    for (int i = 0; i < 8; ++i) v[c][i] = (v[c][i] - mean) * rstd;
+    if (weight) {
+      load8_f32(weight, p.a.weight_dtype, 0, d, D, p.vw, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= e[i] + one;
+    }
+    if (bias) {
+      load8_f32(bias, p.a.weight_dtype, 0, d, D, p.vw, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] += e[i];
     }
   }
 }
 
-template <int NCH>
-__global__ void __launch_bounds__(NCH == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ Params p) {
-  __shared__ float red[4][32];
+// XS, BS: bytes of x's and the block's elements (0: no block).
+// MIN: CTAs that an SM is to hold.
+template <int XS, int BS, int NCH, int MAXT, int MIN>
+__global__ void __launch_bounds__(MAXT, MIN) norm_kernel(const __grid_constant__ Params p) {
+  __shared__ float red[2][4][32];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const mobi_norm_args& a = p.a;
   const int tpr = p.tpr, D = (int)a.D;
-  const int64_t t = tpr == 32 ? (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  const int rows = tpr == 32 ? blockDim.x / 32 : 1;  // rows of a CTA at a time
+  const int64_t stride = (int64_t)gridDim.x * rows;
+  int64_t t = (int64_t)blockIdx.x * rows + (tpr == 32 ? threadIdx.x >> 5 : 0);
   const int l = tpr == 32 ? (threadIdx.x & 31) : threadIdx.x;
   if (t >= a.T) return;  // whole warps, and only where a row is one warp
+  const float inv = 1.0f / (float)D;
 
-  // Every load of the row is issued before the first sum waits for one.
-  Raw8 rx[NCH], rb[NCH];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int d = (c * tpr + l) * 8;
-    if (a.block) rb[c] = load8(a.block, a.block_dtype, t * a.ldb, d, D, p.vb);
-    rx[c] = load8(a.x, a.x_dtype, t * a.ldx, d, D, p.vx);
-  }
-  float r[NCH][8];
-  if (a.block) {
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) widen8(rb[c], a.block_dtype, r[c]);
-    if (a.post != MOBI_NORM_NONE || a.post_weight || a.post_bias)
-      norm_row<NCH>(r, a.post, a.post_eps, a.post_weight, a.post_bias, p, l, red, 0);
+  constexpr int BE = BS ? BS : 2;
+  Raw8<XS> rx[NCH];
+  Raw8<BE> rb[NCH];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int d = (c * tpr + l) * 8;
-      float x[8], g[8];
-      widen8(rx[c], a.x_dtype, x);
-      if (a.gate) {
-        if (a.gate_sd == 1) {
-          widen8(load8(a.gate, a.gate_dtype, t * a.gate_st, d, D, p.vg), a.gate_dtype, g);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int64_t at = t * a.gate_st + (int64_t)(d + i < D ? d + i : 0) * a.gate_sd;
-            g[i] = a.gate_dtype == MOBI_F32    ? static_cast<const float*>(a.gate)[at]
-                   : a.gate_dtype == MOBI_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.gate)[at])
-                                               : to_f32(static_cast<const __half*>(a.gate)[at]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] *= g[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[c][i] = d + i < D ? fmaf(a.scale, r[c][i], x[i]) : 0.0f;
-      if (a.r_out) store8(a.r_out, a.x_dtype, t * a.ldr, d, D, p.vr, r[c]);
+      if constexpr (BS != 0) rb[c] = load8<BE>(a.block, row * a.ldb, d, D, p.vb);
+      rx[c] = load8<XS>(a.x, row * a.ldx, d, D, p.vx);
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) widen8(rx[c], a.x_dtype, r[c]);
-  }
+  };
+  fetch(t);
 
-  norm_row<NCH>(r, a.kind, a.eps, a.weight, a.bias, p, l, red, 2);
-  if (a.out_dtype != MOBI_E4M3) {
+  for (int par = 0; t < a.T; t += stride, par ^= 1) {  // sums of consecutive rows use their own shared rows
+    float r[NCH][8];
+    if constexpr (BS != 0) {
+      Raw8<XS> cx[NCH];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) store8(a.n_out, a.out_dtype, t * a.ldn, (c * tpr + l) * 8, D, p.vn, r[c]);
-    return;
-  }
-  uint8_t* q = static_cast<uint8_t*>(a.n_out) + t * a.ldn;
+      for (int c = 0; c < NCH; ++c) {
+        widen8<BE>(rb[c], a.block_dtype, r[c]);
+        cx[c] = rx[c];
+      }
+      if (t + stride < a.T) fetch(t + stride);
+      if (a.post != MOBI_NORM_NONE || a.post_weight || a.post_bias)
+        norm_row<NCH>(r, a.post, a.post_eps, a.post_weight, a.post_bias, p, l, inv, red[par], 0);
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int d = (c * tpr + l) * 8;
-    uint32_t m = 0;
+      for (int c = 0; c < NCH; ++c) {
+        const int d = (c * tpr + l) * 8;
+        if (a.gate) {
+          float g[8];
+          if (a.gate_sd == 1) {
+            load8_f32(a.gate, a.gate_dtype, t * a.gate_st, d, D, p.vg, g);
+          } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (d + i < D) m = max(m, abs_bits(r[c][i]));
+            for (int i = 0; i < 8; ++i) {
+              const int64_t at = t * a.gate_st + (int64_t)(d + i < D ? d + i : 0) * a.gate_sd;
+              g[i] = a.gate_dtype == MOBI_F32    ? static_cast<const float*>(a.gate)[at]
+                     : a.gate_dtype == MOBI_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.gate)[at])
+                                                 : to_f32(static_cast<const __half*>(a.gate)[at]);
+            }
+          }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (d >= D) continue;
-    const float s = block_scale(m), inv = 1.0f / s;
-    if ((l & 15) == 0) a.n_scale[(int64_t)(d / 128) * a.T + t] = s;
-    const uint32_t lo = e4m3x2(r[c][0] * inv, r[c][1] * inv) | (e4m3x2(r[c][2] * inv, r[c][3] * inv) << 16);
-    const uint32_t hi = e4m3x2(r[c][4] * inv, r[c][5] * inv) | (e4m3x2(r[c][6] * inv, r[c][7] * inv) << 16);
-    if (p.vn && d + 8 <= D) {
-      *reinterpret_cast<uint2*>(q + d) = make_uint2(lo, hi);
+          for (int i = 0; i < 8; ++i) r[c][i] *= g[i];
+        }
+        float x[8];
+        widen8<XS>(cx[c], a.x_dtype, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[c][i] = fmaf(a.scale, r[c][i], x[i]);
+        if (d + 8 > D) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (d + i >= D) r[c][i] = 0.0f;
+        }
+        if (a.r_out) store8(a.r_out, a.x_dtype, t * a.ldr, d, D, p.vr, r[c]);
+      }
     } else {
 #pragma unroll
+      for (int c = 0; c < NCH; ++c) widen8<XS>(rx[c], a.x_dtype, r[c]);
+      if (t + stride < a.T) fetch(t + stride);
+    }
+
+    norm_row<NCH>(r, a.kind, a.eps, a.weight, a.bias, p, l, inv, red[par], 2);
+    if (a.out_dtype != MOBI_E4M3) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) store8(a.n_out, a.out_dtype, t * a.ldn, (c * tpr + l) * 8, D, p.vn, r[c]);
+      continue;
+    }
+    uint8_t* q = static_cast<uint8_t*>(a.n_out) + t * a.ldn;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int d = (c * tpr + l) * 8;
+      uint32_t m = 0;
+#pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (d + i < D) q[d + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        if (d + i < D) m = max(m, abs_bits(r[c][i]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (d >= D) continue;
+      const float s = block_scale(m), f = 1.0f / s;
+      if ((l & 15) == 0) a.n_scale[(int64_t)(d / 128) * a.T + t] = s;
+      const uint32_t lo = e4m3x2(r[c][0] * f, r[c][1] * f) | (e4m3x2(r[c][2] * f, r[c][3] * f) << 16);
+      const uint32_t hi = e4m3x2(r[c][4] * f, r[c][5] * f) | (e4m3x2(r[c][6] * f, r[c][7] * f) << 16);
+      if (p.vn && d + 8 <= D) {
+        *reinterpret_cast<uint2*>(q + d) = make_uint2(lo, hi);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (d + i < D) q[d + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      }
     }
   }
 }
 
-constexpr int kMaxD = 16384;  // 512 threads x 4 chunks x 8 values
+constexpr int kMaxD = 16384;  // 512 threads x 4 octets
+
+// ---- aligned rows ------------------------------------------------------------------
+//
+// The same steps where every row is 16-byte aligned and D is a multiple of 8,
+// with the types of x and the block known to the compiler and values in pairs.
+// The general kernel spends about 70 instructions on a value and is bound by
+// them; this one about 20, which leaves memory as the bound (T = 8192, D = 4096, bf16,
+// norms on both sides, gate, e4m3 out: FAST_FIG).
+
+struct Oct {
+  float2 v[4];
+};
+
+// Octet of type DT (a mobi_dtype) at p.
+template <int DT>
+struct RawOct {
+  uint4 w[DT == MOBI_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p) {
+    w[0] = *static_cast<const uint4*>(p);
+    if constexpr (DT == MOBI_F32) w[1] = static_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() {
+    w[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (DT == MOBI_F32) w[1] = w[0];
+  }
+  __device__ __forceinline__ Oct widen() const {
+    Oct o;
+    if constexpr (DT == MOBI_F32) {
+      o.v[0] = make_float2(__uint_as_float(w[0].x), __uint_as_float(w[0].y));
+      o.v[1] = make_float2(__uint_as_float(w[0].z), __uint_as_float(w[0].w));
+      o.v[2] = make_float2(__uint_as_float(w[1].x), __uint_as_float(w[1].y));
+      o.v[3] = make_float2(__uint_as_float(w[1].z), __uint_as_float(w[1].w));
+    } else {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == MOBI_BF16) o.v[i] = make_float2(bf16lo(u[i]), bf16hi(u[i]));
+        else o.v[i] = make_float2(elem_f32<__half>((uint16_t)u[i]), elem_f32<__half>((uint16_t)(u[i] >> 16)));
+      }
+    }
+    return o;
+  }
+};
+
+__device__ __forceinline__ Oct load_oct(const void* base, int dtype, int64_t at) {
+  if (dtype == MOBI_F32) {
+    RawOct<MOBI_F32> r;
+    r.load(static_cast<const float*>(base) + at);
+    return r.widen();
+  }
+  const uint16_t* q = static_cast<const uint16_t*>(base) + at;
+  if (dtype == MOBI_BF16) {
+    RawOct<MOBI_BF16> r;
+    r.load(q);
+    return r.widen();
+  }
+  RawOct<MOBI_F16> r;
+  r.load(q);
+  return r.widen();
+}
+
+__device__ __forceinline__ void store_oct(void* base, int dtype, int64_t at, const Oct& o) {
+  if (dtype == MOBI_F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    q[0] = make_float4(o.v[0].x, o.v[0].y, o.v[1].x, o.v[1].y);
+    q[1] = make_float4(o.v[2].x, o.v[2].y, o.v[3].x, o.v[3].y);
+    return;
+  }
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dtype == MOBI_BF16) {
+      const __nv_bfloat162 h = __float22bfloat162_rn(o.v[i]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __float22half2_rn(o.v[i]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Sum over the threads of a row (at most 16 warps); `slot` as in row_sum, its unused entries are zero.
+__device__ __forceinline__ float row_sum16(float v, int tpr, float4* slot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tpr == 32) return v;
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(slot)[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float4 a = slot[0], b = slot[1];
+  v = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  if (tpr > 256) {
+    a = slot[2];
+    b = slot[3];
+    v += ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  }
+  return v;
+}
+
+template <int NCH>
+__device__ __forceinline__ void norm_octs(Oct (&r)[NCH], int kind, float eps, const void* weight, const void* bias,
+                                          const Params& p, int l, float inv, float4 (*red)[4]) {
+  const int D = (int)p.a.D, tpr = p.tpr;
+  if (kind == MOBI_NORM_LAYER) {
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, r[c].v[i]);
+    const float mean = row_sum16(s.x + s.y, tpr, red[0]) * inv;
+    const float2 neg = make_float2(-mean, -mean);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if ((c * tpr + l) * 8 < D) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[c].v[i] = __fadd2_rn(r[c].v[i], neg);
+      }
+  }
+  float2 rstd = make_float2(1.0f, 1.0f);
+  if (kind != MOBI_NORM_NONE) {
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = __ffma2_rn(r[c].v[i], r[c].v[i], s);
+    rstd.x = rstd.y = root(row_sum16(s.x + s.y, tpr, red[1]) * inv + eps);
+  }
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int d = (c * tpr + l) * 8;
+    if (d >= D) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[c].v[i] = __fmul2_rn(r[c].v[i], rstd);
+    if (weight) {
+      Oct w = load_oct(weight, p.a.weight_dtype, d);
+      if (p.a.unit_offset) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.v[i] = __fadd2_rn(w.v[i], make_float2(1.0f, 1.0f));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[c].v[i] = __fmul2_rn(r[c].v[i], w.v[i]);
+    }
+    if (bias) {
+      const Oct b = load_oct(bias, p.a.weight_dtype, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[c].v[i] = __fadd2_rn(r[c].v[i], b.v[i]);
+    }
+  }
+}
+
+// XT, BT: types of x and of the block (-1: no block).
+template <int XT, int BT, int NCH, int MAXT, int MIN>
+__global__ void __launch_bounds__(MAXT, MIN) norm_aligned_kernel(const __grid_constant__ Params p) {
+  __shared__ float4 red[2][4][4];
+  if (threadIdx.x < 32) red[threadIdx.x >> 4][(threadIdx.x >> 2) & 3][threadIdx.x & 3] = make_float4(0, 0, 0, 0);
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
+  const mobi_norm_args& a = p.a;
+  const int tpr = p.tpr, D = (int)a.D;
+  const int rows = tpr == 32 ? blockDim.x / 32 : 1;
+  const int64_t stride = (int64_t)gridDim.x * rows;
+  int64_t t = (int64_t)blockIdx.x * rows + (tpr == 32 ? threadIdx.x >> 5 : 0);
+  const int l = tpr == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  if (t >= a.T) return;  // whole warps, and only where a row is one warp
+  const float inv = 1.0f / (float)D;
+  const float2 scale = make_float2(a.scale, a.scale);
+
+  constexpr int XB = XT == MOBI_F32 ? 4 : 2, BB = BT == MOBI_F32 ? 4 : 2;
+  RawOct<XT> rx[NCH];
+  RawOct<BT < 0 ? MOBI_BF16 : BT> rb[NCH];
+  auto fetch = [&](int64_t row) {
+    const uint8_t* px = static_cast<const uint8_t*>(a.x) + row * a.ldx * XB;
+    const uint8_t* pb = BT < 0 ? nullptr : static_cast<const uint8_t*>(a.block) + row * a.ldb * BB;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int d = (c * tpr + l) * 8;
+      if (d < D) {
+        if constexpr (BT >= 0) rb[c].load(pb + d * BB);
+        rx[c].load(px + d * XB);
+      } else {
+        if constexpr (BT >= 0) rb[c].zero();
+        rx[c].zero();
+      }
+    }
+  };
+  fetch(t);
+  for (int par = 0; t < a.T; t += stride, par ^= 1) {
+    Oct r[NCH];
+    if constexpr (BT >= 0) {
+      RawOct<XT> cx[NCH];
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        r[c] = rb[c].widen();
+        cx[c] = rx[c];
+      }
+      if (t + stride < a.T) fetch(t + stride);
+      if (a.post != MOBI_NORM_NONE || a.post_weight || a.post_bias)
+        norm_octs<NCH>(r, a.post, a.post_eps, a.post_weight, a.post_bias, p, l, inv, red[par]);
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int d = (c * tpr + l) * 8;
+        if (d >= D) break;
+        if (a.gate) {
+          Oct g;
+          if (a.gate_sd == 1) {
+            g = load_oct(a.gate, a.gate_dtype, t * a.gate_st + d);
+          } else {  // one value for the row
+            const int64_t at = t * a.gate_st;
+            const float f = a.gate_dtype == MOBI_F32    ? static_cast<const float*>(a.gate)[at]
+                            : a.gate_dtype == MOBI_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.gate)[at])
+                                                        : to_f32(static_cast<const __half*>(a.gate)[at]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g.v[i] = make_float2(f, f);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[c].v[i] = __fmul2_rn(r[c].v[i], g.v[i]);
+        }
+        const Oct x = cx[c].widen();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[c].v[i] = __ffma2_rn(scale, r[c].v[i], x.v[i]);
+        if (a.r_out) store_oct(a.r_out, XT, t * a.ldr + d, r[c]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) r[c] = rx[c].widen();
+      if (t + stride < a.T) fetch(t + stride);
+    }
+
+    norm_octs<NCH>(r, a.kind, a.eps, a.weight, a.bias, p, l, inv, red[par] + 2);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int d = (c * tpr + l) * 8;
+      if (a.out_dtype != MOBI_E4M3) {
+        if (d < D) store_oct(a.n_out, a.out_dtype, t * a.ldn + d, r[c]);
+        continue;
+      }
+      float m = 0.0f;
+      if (d < D) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, r[c].v[i].x), r[c].v[i].y);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (d >= D) continue;
+      const float s = block_scale(__float_as_uint(m)), f = __frcp_rn(s);
+      if ((l & 15) == 0) a.n_scale[(int64_t)(d / 128) * a.T + t] = s;
+      const float2 f2 = make_float2(f, f);
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = __fmul2_rn(r[c].v[i], f2);
+        u[i] = e4m3x2(y.x, y.y);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.n_out) + t * a.ldn + d) =
+          make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
+    }
+  }
+}
+
+// `few`: one octet per thread, so that a row's latency is one load deep; else
+// two, since sums and scales cost a thread the same for sixteen values as for
+// eight. Four past D = 8192. As many CTAs as run at once.
+template <typename Go>
+static cudaError_t plan_rows(Params& p, bool few, Go go) {
+  const int64_t T = p.a.T, oct = (p.a.D + 7) / 8;
+  const int nch = oct > 1024 ? 4 : (oct > 512 || (!few && oct > 32) ? 2 : 1);
+  p.tpr = (int)((oct + 32 * nch - 1) / (32 * nch)) * 32;
+  const int threads = p.tpr == 32 ? 128 : p.tpr, rows = p.tpr == 32 ? 4 : 1;
+  return go(nch, threads, (T + rows - 1) / rows);
+}
+
+template <int XT, int BT>
+static cudaError_t launch_aligned(Params& p, cudaStream_t stream) {
+  return plan_rows(p, p.a.T < 4 * (int64_t)num_sms(), [&](int nch, int threads, int64_t need) {
+    auto run = [&](auto kernel, int maxt, int min) {
+      const int64_t most = (int64_t)num_sms() * (min * maxt / threads);
+      return launch_dependent(kernel, dim3((unsigned)(need < most ? need : most)), threads, 0, 1, stream, p);
+    };
+    if (nch == 1) return run(norm_aligned_kernel<XT, BT, 1, 512, 2>, 512, 2);
+    if (nch == 2 && threads <= 256) return run(norm_aligned_kernel<XT, BT, 2, 256, 3>, 256, 3);
+    if (nch == 2) return run(norm_aligned_kernel<XT, BT, 2, 512, 1>, 512, 1);
+    return run(norm_aligned_kernel<XT, BT, 4, 512, 1>, 512, 1);
+  });
+}
+
+template <int XT>
+static cudaError_t launch_aligned_x(Params& p, cudaStream_t stream) {
+  if (!p.a.block) return launch_aligned<XT, -1>(p, stream);
+  if (p.a.block_dtype == MOBI_F32) return launch_aligned<XT, MOBI_F32>(p, stream);
+  if (p.a.block_dtype == MOBI_BF16) return launch_aligned<XT, MOBI_BF16>(p, stream);
+  return launch_aligned<XT, MOBI_F16>(p, stream);
+}
+
+template <int XS, int BS>
+static cudaError_t launch_types(Params& p, cudaStream_t stream) {
+  return plan_rows(p, true, [&](int nch, int threads, int64_t need) {
+    auto run = [&](auto kernel, int min) {
+      const int64_t most = (int64_t)num_sms() * (min * 512 / threads);
+      return launch_dependent(kernel, dim3((unsigned)(need < most ? need : most)), threads, 0, 1, stream, p);
+    };
+    if (nch == 1) return run(norm_kernel<XS, BS, 1, 512, 2>, 2);
+    if (nch == 2) return run(norm_kernel<XS, BS, 2, 512, 1>, 1);
+    return run(norm_kernel<XS, BS, 4, 512, 1>, 1);
+  });
+}
 
 static cudaError_t launch(Params& p, cudaStream_t stream) {
-  const int64_t T = p.a.T, oct = (p.a.D + 7) / 8;
-  // Few rows: one octet per thread (up to 1024 threads), so that a row's latency
-  // is one load deep. Many rows: two, which keeps more bytes in flight per
-  // thread and needs half the warps at the row's barriers; four past D = 8192.
-  const int nch = oct > 1024 ? 4 : (T >= 2 * num_sms() && oct > 32 ? 2 : 1);
-  const int64_t tpr = ((oct + nch - 1) / nch + 31) / 32 * 32;
-  p.tpr = (int)tpr;
-  const int threads = tpr == 32 ? 256 : (int)tpr;
-  const int64_t grid = tpr == 32 ? (T + 7) / 8 : T;
-  const dim3 g((unsigned)grid);
-  if (nch == 1) return launch_dependent(norm_kernel<1>, g, threads, 0, 1, stream, p);
-  if (nch == 2) return launch_dependent(norm_kernel<2>, g, threads, 0, 1, stream, p);
-  return launch_dependent(norm_kernel<4>, g, threads, 0, 1, stream, p);
+  const mobi_norm_args& a = p.a;
+  if (a.D % 8 == 0 && p.vx && p.vn && p.vw && (!a.block || p.vb) && (!a.r_out || p.vr) &&
+      (!a.gate || a.gate_sd == 0 || (a.gate_sd == 1 && p.vg))) {
+    if (a.x_dtype == MOBI_F32) return launch_aligned_x<MOBI_F32>(p, stream);
+    if (a.x_dtype == MOBI_BF16) return launch_aligned_x<MOBI_BF16>(p, stream);
+    return launch_aligned_x<MOBI_F16>(p, stream);
+  }
+  const bool wide = p.a.x_dtype == MOBI_F32;
+  if (!p.a.block) return wide ? launch_types<4, 0>(p, stream) : launch_types<2, 0>(p, stream);
+  if (p.a.block_dtype == MOBI_F32) return wide ? launch_types<4, 4>(p, stream) : launch_types<2, 4>(p, stream);
+  return wide ? launch_types<4, 2>(p, stream) : launch_types<2, 2>(p, stream);
 }
 
 bool plain_type(int t) { return t >= MOBI_F32 && t <= MOBI_F16; }

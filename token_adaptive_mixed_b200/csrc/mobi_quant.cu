@@ -15,32 +15,62 @@ namespace mobi {
 
 namespace qz {
 
-// Eight values of a row starting at column k (zeros from K on), as fp32.
-template <typename E, bool VEC>
-__device__ __forceinline__ void load8(const E* row, int64_t k, int64_t K, float (&v)[8]) {
-  if (VEC && k + 8 <= K) {
+// Eight values of a row starting at column k (zeros from K on), as stored.
+template <typename E>
+struct Oct {
+  uint32_t w[2 * sizeof(E)];
+
+  // The largest |x| as an fp32 bit pattern. 16-bit patterns of |x| order as integers too, so pairs are reduced as stored.
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t a = 0;
     if constexpr (sizeof(E) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(row + k);
-      const float4 b = *reinterpret_cast<const float4*>(row + k + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = max(a, w[i] & 0x7fffffffu);
+      return a;
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(row + k);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a = __vmaxu2(a, w[i] & 0x7fff7fffu);
+      return abs_bits(elem_f32<E>((uint16_t)max(a & 0xffffu, a >> 16)));
+    }
+  }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    if constexpr (sizeof(E) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = elem_f32<E>((uint16_t)w[i]);
         v[2 * i + 1] = elem_f32<E>((uint16_t)(w[i] >> 16));
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? to_f32(row[k + i]) : 0.0f;
   }
+};
+
+template <typename E, bool VEC>
+__device__ __forceinline__ Oct<E> load8(const E* row, int64_t k, int64_t K) {
+  Oct<E> o;
+  if (VEC && k + 8 <= K) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + k);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i) reinterpret_cast<uint4*>(o.w)[i] = p[i];
+    return o;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * (int)sizeof(E); ++i) o.w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (k + i < K) {
+      if constexpr (sizeof(E) == 4) o.w[i] = reinterpret_cast<const uint32_t*>(row)[k + i];
+      else o.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k + i] << (16 * (i & 1));
+    }
+  return o;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(uint8_t* row, int64_t k, int64_t K, const float (&v)[8], float r) {
+template <typename E, bool VEC>
+__device__ __forceinline__ void store8(uint8_t* row, int64_t k, int64_t K, const Oct<E>& o, float r) {
+  float v[8];
+  o.widen(v);
   uint32_t lo = e4m3x2(v[0] * r, v[1] * r) | (e4m3x2(v[2] * r, v[3] * r) << 16);
   uint32_t hi = e4m3x2(v[4] * r, v[5] * r) | (e4m3x2(v[6] * r, v[7] * r) << 16);
   if (VEC && k + 8 <= K) {
@@ -50,13 +80,6 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t k, int64_t K, const
     for (int i = 0; i < 8; ++i)
       if (k + i < K) row[k + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
   }
-}
-
-__device__ __forceinline__ uint32_t max8(const float (&v)[8]) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
-  return a;
 }
 
 constexpr int kThreads = 256;
@@ -74,18 +97,18 @@ __global__ void __launch_bounds__(kThreads) quant_row_kernel(const E* X, int64_t
   const int l = threadIdx.x & 15;
   if (t >= T) return;  // whole half-warps
   const unsigned mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
-  float v[kRowBlocks][8];
+  Oct<E> v[kRowBlocks];
 #pragma unroll
-  for (int b = 0; b < kRowBlocks; ++b) load8<E, VEC>(X + t * ldx, (kb0 + b) * 128 + 8 * l, K, v[b]);
+  for (int b = 0; b < kRowBlocks; ++b) v[b] = load8<E, VEC>(X + t * ldx, (kb0 + b) * 128 + 8 * l, K);
 #pragma unroll
   for (int b = 0; b < kRowBlocks; ++b) {
     if (kb0 + b >= nkb) break;
-    uint32_t a = max8(v[b]);
+    uint32_t a = v[b].amax();
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(mask, a, o));
     const float s = block_scale(a);
     if (l == 0) scale[(kb0 + b) * T + t] = s;
-    store8<VEC>(Q + t * ldq, (kb0 + b) * 128 + 8 * l, K, v[b], 1.0f / s);
+    store8<E, VEC>(Q + t * ldq, (kb0 + b) * 128 + 8 * l, K, v[b], 1.0f / s);
   }
 }
 
@@ -99,20 +122,12 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const E* X, int64
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t nkb = (K + 127) / 128, kb = blockIdx.x % nkb, rb = blockIdx.x / nkb;
   const int64_t k = kb * 128 + 8 * (threadIdx.x & 15), t0 = rb * 128 + (threadIdx.x >> 4);
-  float v[8][8];
+  Oct<E> v[8];
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t t = t0 + 16 * i;
-    if (t < T) {
-      load8<E, VEC>(X + t * ldx, k, K, v[i]);
-    } else {
+  for (int i = 0; i < 8; ++i) v[i] = load8<E, VEC>(X + (t0 + 16 * i) * ldx, k, t0 + 16 * i < T ? K : 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, max8(v[i]));
+  for (int i = 0; i < 8; ++i) a = max(a, v[i].amax());
   a = __reduce_max_sync(0xffffffffu, a);
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = a;
   __syncthreads();
@@ -122,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const E* X, int64
   if (threadIdx.x == 0) scale[kb * ((T + 127) / 128) + rb] = s;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (t0 + 16 * i < T) store8<VEC>(Q + (t0 + 16 * i) * ldq, k, K, v[i], r);
+    if (t0 + 16 * i < T) store8<E, VEC>(Q + (t0 + 16 * i) * ldq, k, K, v[i], r);
 }
 
 template <typename E, bool VEC>
