@@ -6,14 +6,23 @@
 //   logprob = (x_target - m) / temperature - ln S,   entropy = ln S - ln 2 * W / S
 // one pass over the row in fp32, no logarithm per element.
 //
+// An entry of -infinity is counted as "floor" (-1e30, or fp16's lowest), which
+// spares a guard against 0 * infinity per value; with the running maximum
+// starting there too, such entries vanish once a real one is seen. A part
+// whose maximum is not far above the floor is summed again, value by value.
+// Values are taken in pairs: about six instructions each, of which the
+// exponential's unit is the next bound (bf16).
+//
 // Top alternatives without a second pass over the row: neighbouring threads
 // form 128 groups, and the k-th largest of the groups' maxima (k <= 32) is a bound tau
 // that at least k entries reach. Only groups whose maximum reaches it can hold
 // one, so about k/128 of the row is read again (from L2), the entries >= tau are
-// gathered and ranked. Many equal entries (a mask of the type's lowest value,
-// constant rows) would overflow the gather: then the entries above tau are
-// gathered and the first ones equal to it are found in index order; where even
-// those overflow, k searches over the whole row remain.
+// gathered and ranked. Many equal entries would overflow the gather: then the
+// entries above tau are gathered and the first ones equal to it are found in
+// index order. Where that does not do (even those overflow, or fewer than k
+// groups have an entry above the floor, as under a mask of the type's lowest
+// value), the row is searched for the next lower value and its first entries
+// until there are k.
 //
 // Few rows: a cluster of up to eight CTAs shares a row; CTA 0 joins their
 // statistics and candidates through distributed shared memory, in rank order.
@@ -27,11 +36,29 @@ namespace mobi {
 
 namespace lp {
 
-constexpr int kThreads = 512;
-constexpr int kGroups = 128, kPerGroup = kThreads / kGroups;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Group g is the threads 32 (g / 16) + g % 16 and the same + 16: lanes l and l + 16 of a warp.
+constexpr int kGroups = kThreads / 2;
 constexpr int kMaxK = 32;
 constexpr int kCap = 1024;   // gathered candidates
 constexpr float kLowest = -3.402823466e38f;
+
+// What -infinity counts as, and the same as a pair of 16-bit patterns.
+template <typename E>
+struct Floor {
+  static constexpr float value = -1.0e30f;  // fp32
+};
+template <>
+struct Floor<__nv_bfloat16> {
+  static constexpr uint32_t pair = 0xf149f149u;
+  static constexpr float value = -9.95303792e+29f;  // 0xf149
+};
+template <>
+struct Floor<__half> {
+  static constexpr uint32_t pair = 0xfbfffbffu;
+  static constexpr float value = -65504.0f;
+};
 
 struct Stat {
   float m, s, w;
@@ -54,7 +81,63 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
   return r;
 }
 
-// Adds N values (fp32) to a running state.
+// max(a, b, c), ignoring NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Adds the 16 bytes `r` of logits to a running state that starts at the floor.
+template <typename E>
+__device__ __forceinline__ void add_pairs(Stat& a, const uint4& r, float c) {
+  constexpr int P = 8 / sizeof(E);  // pairs
+  float2 x[P];
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      x[i] = make_float2(max_nan(__uint_as_float(w[2 * i]), Floor<E>::value),
+                         max_nan(__uint_as_float(w[2 * i + 1]), Floor<E>::value));
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      uint32_t v;
+      if constexpr (sizeof(E) == 2 && Floor<E>::pair == Floor<__half>::pair)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(v) : "r"(w[i]), "r"(Floor<E>::pair));
+      else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(w[i]), "r"(Floor<E>::pair));
+      x[i] = make_float2(elem_f32<E>((uint16_t)v), elem_f32<E>((uint16_t)(v >> 16)));
+    }
+  }
+  float m = a.m;
+#pragma unroll
+  for (int i = 0; i < P; ++i) m = max3(m, x[i].x, x[i].y);
+  if (m > a.m) {
+    const float d = (a.m - m) * c, f = ex2(d);
+    a.w = f > 0.0f ? f * fmaf(d, a.s, a.w) : 0.0f;
+    a.s *= f;
+    a.m = m;
+  }
+  const float2 neg = make_float2(-a.m, -a.m), c2 = make_float2(c, c);
+  float2 s = make_float2(0.0f, 0.0f), t = s;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const float2 v = __fmul2_rn(__fadd2_rn(x[i], neg), c2);
+    const float2 e = make_float2(ex2(v.x), ex2(v.y));
+    s = __fadd2_rn(s, e);
+    t = __ffma2_rn(e, v, t);
+  }
+  a.s += s.x + s.y;
+  a.w += t.x + t.y;
+}
+
+// Adds N values (fp32) to a running state that starts at {kLowest, 0, 0}.
 template <int N>
 __device__ __forceinline__ void add(Stat& a, const float (&x)[N], float c) {
   float m = x[0];
@@ -132,16 +215,16 @@ __device__ __forceinline__ Part<E> make_part(const E* row, int64_t lo, int64_t h
 }
 
 struct Smem {
-  Stat warp[kThreads / 32];
-  float gmax[kGroups];
+  Stat warp[kWarps];
+  float gmax[kGroups];             // the groups' maxima
   float tau;
-  int n, above, groups;
+  int n, groups;
   int list[kGroups];
-  uint64_t key[kCap];
-  uint64_t best[kThreads / 32];
+  uint64_t key[kCap + kMaxK];
+  float best[kWarps];
   uint64_t top[kMaxK];             // this CTA's part, in order (0: none)
   Stat total;
-  int count[kThreads / 32];
+  int count[kWarps];
 };
 
 __device__ __forceinline__ void push(Smem& sm, float x, int64_t i) {
@@ -160,10 +243,10 @@ __device__ void gather(Smem& sm, const Part<E>& p, float tau, bool strict) {
   if (tid < kGroups && (strict ? sm.gmax[tid] > tau : sm.gmax[tid] >= tau)) sm.list[atomicAdd(&sm.groups, 1)] = tid;
   __syncthreads();
   const int ng = sm.groups, per = (p.chunks + kThreads - 1) / kThreads;  // chunks of a thread
-  for (int g = warp; g < ng; g += kThreads / 32) {
-    const int base = sm.list[g] * kPerGroup;
-    for (int j = lane; j < per * kPerGroup; j += 32) {
-      const int i = (j / kPerGroup) * kThreads + base + j % kPerGroup;
+  for (int g = warp; g < ng; g += kWarps) {
+    const int id = sm.list[g], base = 32 * (id / 16) + id % 16;
+    for (int j = lane; j < 2 * per; j += 32) {
+      const int i = (j >> 1) * kThreads + base + 16 * (j & 1);
       if (i >= p.chunks) continue;
       float x[EC];
       p.chunk(i, x);
@@ -180,96 +263,134 @@ __device__ void gather(Smem& sm, const Part<E>& p, float tau, bool strict) {
   __syncthreads();
 }
 
+// Appends the first `need` entries equal to v, in index order, as candidates n, n + 1, ..; returns how many there were (at most need).
+template <typename E>
+__device__ int first_equal(Smem& sm, const Part<E>& p, float v, int need, int n) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int have = 0;
+  for (int64_t i0 = p.lo; i0 < p.hi && have < need; i0 += kThreads) {
+    const int64_t i = i0 + tid;
+    const bool eq = i < p.hi && to_f32(p.row[i]) == v;
+    const unsigned b = __ballot_sync(0xffffffffu, eq);
+    __syncthreads();
+    if (lane == 0) sm.count[warp] = __popc(b);
+    __syncthreads();
+    int before = have, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm.count[w];
+      all += sm.count[w];
+    }
+    before += __popc(b & ((1u << lane) - 1));
+    if (eq && before < need) sm.key[n + before] = make_key(v, (uint32_t)i);
+    have += all;
+  }
+  __syncthreads();
+  return have < need ? have : need;
+}
+
+// The part's largest entry below `bound` (equal: or equal to it), -infinity if there is none.
+template <typename E>
+__device__ float next_value(Smem& sm, const Part<E>& p, float bound, bool equal) {
+  constexpr int EC = Part<E>::EC;
+  const int tid = threadIdx.x;
+  float best = -INFINITY;
+  for (int i = tid; i < p.chunks; i += kThreads) {
+    float x[EC];
+    p.chunk(i, x);
+#pragma unroll
+    for (int e = 0; e < EC; ++e)
+      if (x[e] < bound || (equal && x[e] == bound)) best = fmaxf(best, x[e]);
+  }
+  if (tid < p.edge()) {
+    const float x = to_f32(p.row[p.edge_at(tid)]);
+    if (x < bound || (equal && x == bound)) best = fmaxf(best, x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+  __syncthreads();
+  if ((tid & 31) == 0) sm.best[tid >> 5] = best;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) best = fmaxf(best, sm.best[w]);
+  return best;
+}
+
 // sm.top[0..k) <- the part's k largest keys in order (0 where there are fewer).
 template <typename E>
 __device__ void top_keys(Smem& sm, const Part<E>& p, int k) {
-  constexpr int EC = Part<E>::EC;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   if (tid < kMaxK) sm.top[tid] = 0;
-  if (tid == 0) sm.tau = kLowest;  // fewer than k groups: every entry above -infinity
   __syncthreads();
-  if (tid < kGroups) {  // the k-th largest group maximum (ties share a rank range; any of them is the bound)
-    const float v = sm.gmax[tid];
+  // The k-th largest group maximum. A warp ranks sixteen groups: lanes l and
+  // l + 16 count one group's larger and equal ones among half of the others each.
+  {
+    const int lane = tid & 31, half = lane >> 4;
+    const float v = sm.gmax[16 * (tid >> 5) + (lane & 15)];
     int more = 0, same = 0;
-    for (int i = 0; i < kGroups; ++i) {
-      const float o = sm.gmax[i];
+#pragma unroll 16
+    for (int i = 0; i < kGroups / 2; ++i) {
+      const float o = sm.gmax[half * (kGroups / 2) + i];
       more += o > v;
       same += o == v;
     }
+    more += __shfl_xor_sync(0xffffffffu, more, 16);
+    same += __shfl_xor_sync(0xffffffffu, same, 16);
     if (more < k && k <= more + same) sm.tau = v;  // equal values only
   }
   __syncthreads();
-  const float tau = sm.tau;
-  gather(sm, p, tau, false);
-  int n = sm.n;
-  if (n > kCap) {
+  const float tau = sm.tau, floor = Floor<E>::value;
+  const bool floored = tau <= floor;  // group maxima at the floor stand for -infinity and for what is below it
+  int n = 0;
+  float bound = INFINITY;
+  bool equal = false, more = true;
+  gather(sm, p, floored ? floor : tau, floored);
+  if (sm.n <= kCap) {
+    n = sm.n;
+    more = floored;
+    bound = floor;
+    equal = true;
+  } else if (!floored) {
     __syncthreads();
     gather(sm, p, tau, true);
-    n = sm.n;
-    const int need = k - n;  // entries equal to tau, lowest indices first
-    if (n <= kCap && need > 0) {
-      int have = 0;
-      for (int64_t i0 = p.lo; i0 < p.hi && have < need; i0 += kThreads) {
-        const int64_t i = i0 + tid;
-        const bool eq = i < p.hi && to_f32(p.row[i]) == tau;
-        const unsigned b = __ballot_sync(0xffffffffu, eq);
-        __syncthreads();
-        if (lane == 0) sm.count[warp] = __popc(b);
-        __syncthreads();
-        int before = have, all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-          if (w < warp) before += sm.count[w];
-          all += sm.count[w];
-        }
-        before += __popc(b & ((1u << lane) - 1));
-        if (eq && before < need && n + before < kCap) sm.key[n + before] = make_key(tau, (uint32_t)i);
-        have += all;
-      }
-      n += have < need ? have : need;
-      __syncthreads();
+    if (sm.n <= kCap) {
+      n = sm.n;
+      bound = tau;
+      equal = true;
     }
   }
-  if (n <= kCap) {
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t key = sm.key[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += sm.key[j] > key;
-      if (rank < k) sm.top[rank] = key;
-    }
-    __syncthreads();
-    return;
+  __syncthreads();
+  while (more && n < k) {
+    const float v = next_value(sm, p, bound, equal);
+    if (v == -INFINITY) break;
+    n += first_equal(sm, p, v, k - n, n);
+    bound = v;
+    equal = false;
   }
-  // k searches: the largest key below the last one.
-  uint64_t last = ~0ull;
-  for (int r = 0; r < k; ++r) {
-    uint64_t best = 0;
-    for (int i = tid; i < p.chunks; i += kThreads) {
-      float x[EC];
-      p.chunk(i, x);
-#pragma unroll
-      for (int e = 0; e < EC; ++e) {
-        const uint64_t key = make_key(x[e], (uint32_t)(p.body + (int64_t)i * EC + e));
-        if (x[e] > -INFINITY && key < last && key > best) best = key;
-      }
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t key = sm.key[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += sm.key[j] > key;
+    if (rank < k) sm.top[rank] = key;
+  }
+  __syncthreads();
+}
+
+// sm.total <- the threads' states joined, in a fixed order.
+__device__ __forceinline__ void block_join(Smem& sm, Stat a, float c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto over = [&](int first) {
+    for (int o = first; o > 0; o >>= 1) {
+      const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                      __shfl_xor_sync(0xffffffffu, a.w, o)};
+      a = join(a, b, c);
     }
-    if (tid < p.edge()) {
-      const int64_t i = p.edge_at(tid);
-      const float x = to_f32(p.row[i]);
-      const uint64_t key = make_key(x, (uint32_t)i);
-      if (x > -INFINITY && key < last && key > best) best = key;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
-      best = v > best ? v : best;
-    }
-    __syncthreads();
-    if (lane == 0) sm.best[warp] = best;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) best = sm.best[w] > best ? sm.best[w] : best;
-    if (best == 0) break;  // uniform
-    if (tid == 0) sm.top[r] = best;
-    last = best;
+  };
+  over(16);
+  if (lane == 0) sm.warp[warp] = a;
+  __syncthreads();
+  if (warp == 0) {
+    a = lane < kWarps ? sm.warp[lane] : Stat{kLowest, 0.0f, 0.0f};
+    over(kWarps / 2);
+    if (lane == 0) sm.total = a;
   }
   __syncthreads();
 }
@@ -287,7 +408,7 @@ __device__ __forceinline__ V remote(const V* p, uint32_t rank) {
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 6)
     logprobs_kernel(const E* logits, int64_t V, int64_t ld, const int64_t* targets, float temperature, int k,
                     int csize, float* logprob, float* entropy, float* top_logprob, int32_t* top_index,
                     DeviceStatus* st) {
@@ -295,59 +416,49 @@ __global__ void __launch_bounds__(kThreads, 3)
   __shared__ Smem sm;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int64_t t = blockIdx.x / csize;
   const int rank = blockIdx.x % csize;
   const E* row = logits + t * ld;
   const float c = 1.44269504088896341f / temperature;
   const Part<E> p = make_part(row, V * rank / csize, V * (rank + 1) / csize);
 
-  Stat a = {kLowest, 0.0f, 0.0f};
+  Stat a = {Floor<E>::value, 0.0f, 0.0f};
   int i = tid;
   for (; i + (U - 1) * kThreads < p.chunks; i += U * kThreads) {
     uint4 r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) r[u] = p.raw(i + u * kThreads);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[EC];
-      Part<E>::widen(r[u], x);
-      add<EC>(a, x, c);
-    }
+    for (int u = 0; u < U; ++u) add_pairs<E>(a, r[u], c);
   }
-  for (; i < p.chunks; i += kThreads) {
-    float x[EC];
-    p.chunk(i, x);
-    add<EC>(a, x, c);
-  }
+  for (; i < p.chunks; i += kThreads) add_pairs<E>(a, p.raw(i), c);
   if (tid < p.edge()) {
-    const float x[1] = {to_f32(row[p.edge_at(tid)])};
+    const float x[1] = {max_nan(to_f32(row[p.edge_at(tid)]), Floor<E>::value)};
     add<1>(a, x, c);
   }
 
   if (k > 0) {
-    float g = a.m;
-#pragma unroll
-    for (int o = kPerGroup / 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if (tid % kPerGroup == 0) sm.gmax[tid / kPerGroup] = g;
+    const float g = fmaxf(a.m, __shfl_xor_sync(0xffffffffu, a.m, 16));
+    if ((tid & 31) < 16) sm.gmax[16 * (tid >> 5) + (tid & 31)] = g;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                    __shfl_xor_sync(0xffffffffu, a.w, o)};
-    a = join(a, b, c);
-  }
-  if (lane == 0) sm.warp[warp] = a;
-  __syncthreads();
-  if (warp == 0) {
-    a = lane < kThreads / 32 ? sm.warp[lane] : Stat{kLowest, 0.0f, 0.0f};
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                      __shfl_xor_sync(0xffffffffu, a.w, o)};
-      a = join(a, b, c);
+  block_join(sm, a, c);
+  // Entries at the floor have to be nothing beside the largest one, and no
+  // exponent may overflow (far larger logits or smaller temperatures than a model's).
+  const float span = (sm.total.m - Floor<E>::value) * c;
+  if (!(span >= 150.0f && span <= 1.0e37f)) {
+    a = Stat{kLowest, 0.0f, 0.0f};
+    for (i = tid; i < p.chunks; i += kThreads) {
+      float x[EC];
+      p.chunk(i, x);
+      add<EC>(a, x, c);
     }
-    if (lane == 0) sm.total = a;
+    if (tid < p.edge()) {
+      const float x[1] = {to_f32(row[p.edge_at(tid)])};
+      add<1>(a, x, c);
+    }
+    __syncthreads();
+    block_join(sm, a, c);
   }
   if (k > 0) top_keys(sm, p, k);
 
