@@ -93,31 +93,45 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Adds the 16 bytes `r` of logits to a running state that starts at the floor.
+// Larger of two pairs of 16-bit values, NaN if either is.
 template <typename E>
-__device__ __forceinline__ void add_pairs(Stat& a, const uint4& r, float c) {
-  constexpr int P = 8 / sizeof(E);  // pairs
-  float2 x[P];
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  if constexpr (sizeof(E) == 4) {
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (Floor<E>::pair == Floor<__half>::pair)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Adds U times 16 bytes of logits to a running state that starts at the floor;
+// one rescaling for all of them.
+template <typename E, int U>
+__device__ __forceinline__ void add_chunks(Stat& a, const uint4 (&r)[U], float c) {
+  uint32_t w[4 * U];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      x[i] = make_float2(max_nan(__uint_as_float(w[2 * i]), Floor<E>::value),
-                         max_nan(__uint_as_float(w[2 * i + 1]), Floor<E>::value));
-  } else {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      uint32_t v;
-      if constexpr (sizeof(E) == 2 && Floor<E>::pair == Floor<__half>::pair)
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(v) : "r"(w[i]), "r"(Floor<E>::pair));
-      else
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(w[i]), "r"(Floor<E>::pair));
-      x[i] = make_float2(elem_f32<E>((uint16_t)v), elem_f32<E>((uint16_t)(v >> 16)));
-    }
+  for (int u = 0; u < U; ++u) {
+    w[4 * u] = r[u].x;
+    w[4 * u + 1] = r[u].y;
+    w[4 * u + 2] = r[u].z;
+    w[4 * u + 3] = r[u].w;
   }
   float m = a.m;
+  if constexpr (sizeof(E) == 4) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) m = max3(m, x[i].x, x[i].y);
+    for (int i = 0; i < 4 * U; ++i) w[i] = __float_as_uint(max_nan(__uint_as_float(w[i]), Floor<E>::value));
+#pragma unroll
+    for (int i = 0; i < 4 * U; i += 2) m = max3(m, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+  } else {
+    // A NaN would carry through the packed maximum into m; it shows in the sums all the same.
+    uint32_t x = Floor<E>::pair;
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) {
+      w[i] = max_pair<E>(w[i], Floor<E>::pair);
+      x = i ? max_pair<E>(x, w[i]) : w[i];
+    }
+    m = max3(m, elem_f32<E>((uint16_t)x), elem_f32<E>((uint16_t)(x >> 16)));
+  }
   if (m > a.m) {
     const float d = (a.m - m) * c, f = ex2(d);
     a.w = f > 0.0f ? f * fmaf(d, a.s, a.w) : 0.0f;
@@ -126,12 +140,18 @@ __device__ __forceinline__ void add_pairs(Stat& a, const uint4& r, float c) {
   }
   const float2 neg = make_float2(-a.m, -a.m), c2 = make_float2(c, c);
   float2 s = make_float2(0.0f, 0.0f), t = s;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const float2 v = __fmul2_rn(__fadd2_rn(x[i], neg), c2);
+  auto one = [&](float2 x) {
+    const float2 v = __fmul2_rn(__fadd2_rn(x, neg), c2);
     const float2 e = make_float2(ex2(v.x), ex2(v.y));
     s = __fadd2_rn(s, e);
     t = __ffma2_rn(e, v, t);
+  };
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4 * U; i += 2) one(make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) one(make_float2(elem_f32<E>((uint16_t)w[i]), elem_f32<E>((uint16_t)(w[i] >> 16))));
   }
   a.s += s.x + s.y;
   a.w += t.x + t.y;
@@ -216,7 +236,7 @@ __device__ __forceinline__ Part<E> make_part(const E* row, int64_t lo, int64_t h
 
 struct Smem {
   Stat warp[kWarps];
-  float gmax[kGroups];             // the groups' maxima
+  alignas(16) float gmax[kGroups];  // the groups' maxima
   float tau;
   int n, groups;
   int list[kGroups];
@@ -245,14 +265,25 @@ __device__ void gather(Smem& sm, const Part<E>& p, float tau, bool strict) {
   const int ng = sm.groups, per = (p.chunks + kThreads - 1) / kThreads;  // chunks of a thread
   for (int g = warp; g < ng; g += kWarps) {
     const int id = sm.list[g], base = 32 * (id / 16) + id % 16;
-    for (int j = lane; j < 2 * per; j += 32) {
-      const int i = (j >> 1) * kThreads + base + 16 * (j & 1);
-      if (i >= p.chunks) continue;
-      float x[EC];
-      p.chunk(i, x);
+    for (int j0 = lane; j0 < 2 * per; j0 += 4 * 32) {
+      uint4 r[4];
+      int at[4];
 #pragma unroll
-      for (int e = 0; e < EC; ++e)
-        if ((strict ? x[e] > tau : x[e] >= tau) && x[e] > -INFINITY) push(sm, x[e], p.body + (int64_t)i * EC + e);
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 32 * u;
+        at[u] = (j >> 1) * kThreads + base + 16 * (j & 1);
+        if (at[u] < p.chunks) r[u] = p.raw(at[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (at[u] >= p.chunks) continue;
+        float x[EC];
+        Part<E>::widen(r[u], x);
+#pragma unroll
+        for (int e = 0; e < EC; ++e)
+          if ((strict ? x[e] > tau : x[e] >= tau) && x[e] > -INFINITY)
+            push(sm, x[e], p.body + (int64_t)at[u] * EC + e);
+      }
     }
   }
   if (tid < p.edge()) {
@@ -326,11 +357,12 @@ __device__ void top_keys(Smem& sm, const Part<E>& p, int k) {
     const int lane = tid & 31, half = lane >> 4;
     const float v = sm.gmax[16 * (tid >> 5) + (lane & 15)];
     int more = 0, same = 0;
-#pragma unroll 16
-    for (int i = 0; i < kGroups / 2; ++i) {
-      const float o = sm.gmax[half * (kGroups / 2) + i];
-      more += o > v;
-      same += o == v;
+    const float4* other = reinterpret_cast<const float4*>(&sm.gmax[half * (kGroups / 2)]);
+#pragma unroll
+    for (int i = 0; i < kGroups / 8; ++i) {
+      const float4 o = other[i];
+      more += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+      same += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
     }
     more += __shfl_xor_sync(0xffffffffu, more, 16);
     same += __shfl_xor_sync(0xffffffffu, same, 16);
@@ -374,21 +406,27 @@ __device__ void top_keys(Smem& sm, const Part<E>& p, int k) {
   __syncthreads();
 }
 
-// sm.total <- the threads' states joined, in a fixed order.
+// sm.total <- the threads' states joined, in a fixed order: the maximum first,
+// then sums of states rescaled to it.
 __device__ __forceinline__ void block_join(Smem& sm, Stat a, float c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto over = [&](int first) {
+    float m = a.m;
+    for (int o = first; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float d = (a.m - m) * c, f = ex2(d);
+    a.w = f > 0.0f ? f * fmaf(d, a.s, a.w) : 0.0f;
+    a.s *= f;
+    a.m = m;
     for (int o = first; o > 0; o >>= 1) {
-      const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                      __shfl_xor_sync(0xffffffffu, a.w, o)};
-      a = join(a, b, c);
+      a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+      a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
     }
   };
   over(16);
   if (lane == 0) sm.warp[warp] = a;
   __syncthreads();
   if (warp == 0) {
-    a = lane < kWarps ? sm.warp[lane] : Stat{kLowest, 0.0f, 0.0f};
+    a = sm.warp[lane % kWarps];
     over(kWarps / 2);
     if (lane == 0) sm.total = a;
   }
@@ -423,16 +461,24 @@ __global__ void __launch_bounds__(kThreads, 6)
   const float c = 1.44269504088896341f / temperature;
   const Part<E> p = make_part(row, V * rank / csize, V * (rank + 1) / csize);
 
+  // The target's logit is on its way while the row is summed.
+  int64_t y = -1;
+  float xt = 0.0f;
+  if (tid == 0 && rank == 0 && targets) {
+    y = targets[t];
+    if (y >= 0 && y < V) xt = to_f32(row[y]);
+  }
   Stat a = {Floor<E>::value, 0.0f, 0.0f};
-  int i = tid;
-  for (; i + (U - 1) * kThreads < p.chunks; i += U * kThreads) {
+  for (int i = tid; i < p.chunks; i += U * kThreads) {
     uint4 r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = p.raw(i + u * kThreads);
-#pragma unroll
-    for (int u = 0; u < U; ++u) add_pairs<E>(a, r[u], c);
+    for (int u = 0; u < U; ++u) {
+      constexpr uint32_t none = sizeof(E) == 4 ? 0xff800000u : (Floor<E>::value == -65504.0f ? 0xfc00fc00u : 0xff80ff80u);
+      r[u] = make_uint4(none, none, none, none);  // -infinity
+      if (i + u * kThreads < p.chunks) r[u] = p.raw(i + u * kThreads);
+    }
+    add_chunks<E, U>(a, r, c);
   }
-  for (; i < p.chunks; i += kThreads) add_pairs<E>(a, p.raw(i), c);
   if (tid < p.edge()) {
     const float x[1] = {max_nan(to_f32(row[p.edge_at(tid)]), Floor<E>::value)};
     add<1>(a, x, c);
@@ -448,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 6)
   const float span = (sm.total.m - Floor<E>::value) * c;
   if (!(span >= 150.0f && span <= 1.0e37f)) {
     a = Stat{kLowest, 0.0f, 0.0f};
-    for (i = tid; i < p.chunks; i += kThreads) {
+    for (int i = tid; i < p.chunks; i += kThreads) {
       float x[EC];
       p.chunk(i, x);
       add<EC>(a, x, c);
@@ -505,13 +551,12 @@ __global__ void __launch_bounds__(kThreads, 6)
   if (tid == 0) {
     if (entropy) entropy[t] = empty ? 0.0f : log_s - 0.693147180559945309f * (a.w / a.s);
     if (targets) {
-      const int64_t y = targets[t];
       float v = 0.0f;
       if (y >= V) {
         v = NAN;
         report_error(st, kErrTargetRange, 0x601);
       } else if (y >= 0) {
-        v = empty ? -INFINITY : (to_f32(row[y]) - a.m) / temperature - log_s;
+        v = empty ? -INFINITY : (xt - a.m) / temperature - log_s;
       }
       logprob[t] = v;
     }
