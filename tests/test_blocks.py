@@ -1,0 +1,136 @@
+"""CPU checks of the 8-bit layer, the norm between blocks and the scoring of
+logits: every refusal happens on the host, before a launch."""
+import ctypes
+
+import pytest
+import torch
+
+import token_adaptive_mixed_b200 as mobi
+from token_adaptive_mixed_b200 import blocks
+from token_adaptive_mixed_b200 import build as mobi_build
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def L():
+    mobi_build.build()
+    return mobi.lib()
+
+
+def test_quant_refusals(L):
+    def call(X=FAKE, dt=1, T=8, K=256, ldx=256, rows=1, Q=FAKE, ldq=256, s=FAKE):
+        return L.mobi_fp8_quant(X, dt, T, K, ldx, rows, Q, ldq, s, None)
+    assert call(T=0) == 0 and call(K=0) == 0
+    assert call(T=-1) == 1 and call(K=-1) == 1
+    assert call(dt=3) == 1 and call(dt=-1) == 1
+    assert call(rows=64) == 1
+    assert call(X=None) == 1 and call(Q=None) == 1 and call(s=None) == 1
+    assert call(ldx=255) == 1 and call(ldq=255) == 1
+    assert call(X=FAKE + 1) == 3 and call(dt=0, X=FAKE + 2) == 3 and call(s=FAKE + 2) == 3
+    assert call(T=1 << 29) == 2 and call(K=1 << 24, ldx=1 << 24, ldq=1 << 24) == 2
+    assert call(T=1 << 28, K=1 << 28, ldx=1 << 28, ldq=1 << 28, rows=128) == 2
+
+
+def test_gemm_refusals(L):
+    def call(X=FAKE, ldx=256, xs=FAKE, T=8, K=256, W=FAKE, ldw=256, ws=FAKE, N=64, dt=0, Y=FAKE, ldy=64):
+        return L.mobi_fp8_gemm(X, ldx, xs, T, K, W, ldw, ws, N, dt, Y, ldy, None)
+    assert call(T=0) == 0 and call(N=0) == 0
+    assert call(T=-1) == 1 and call(N=-1) == 1 and call(K=-1) == 1
+    assert call(K=0) == 2 and call(T=1 << 29) == 2
+    assert call(dt=3) == 1 and call(dt=4) == 1
+    for k in ("X", "xs", "W", "ws", "Y"):
+        assert call(**{k: None}) == 1, k
+    assert call(ldx=240) == 1 and call(ldw=240) == 1 and call(ldy=63) == 1
+    assert call(X=FAKE + 8) == 3 and call(W=FAKE + 8) == 3 and call(ldx=264) == 3 and call(ldw=264) == 3
+    assert call(xs=FAKE + 2) == 3 and call(Y=FAKE + 2) == 3 and call(dt=1, Y=FAKE + 1) == 3
+
+
+def test_gated_refusals(L):
+    def call(X=FAKE, xs=FAKE, T=8, K=256, Wg=FAKE, gs=FAKE, Wu=FAKE, us=FAKE, N=64, act=0, dt=1, H=FAKE, ldh=64,
+             hs=FAKE, ldu=256):
+        return L.mobi_fp8_gated(X, 256, xs, T, K, Wg, 256, gs, Wu, ldu, us, N, act, dt, H, ldh, hs, None)
+    assert call(T=0) == 0 and call(N=0) == 0
+    assert call(act=4) == 1 and call(act=-1) == 1 and call(dt=4) == 1 and call(dt=-1) == 1
+    for k in ("X", "xs", "Wg", "gs", "Wu", "us", "H"):
+        assert call(**{k: None}) == 1, k
+    assert call(dt=3, hs=None) == 1 and call(dt=3, hs=FAKE + 2) == 3
+    assert call(ldu=250) == 1 and call(Wu=FAKE + 4) == 3 and call(ldh=63) == 1
+
+
+def test_norm_refusals(L):
+    def call(**kw):
+        a = blocks.NormArgs()
+        d = dict(x=FAKE, n_out=FAKE, T=4, D=64, ldx=64, ldn=64, kind=1, eps=1e-6, x_dtype=1, out_dtype=1)
+        for k, v in {**d, **kw}.items():
+            setattr(a, k, v)
+        return L.mobi_norm(ctypes.addressof(a), None)
+    blk = dict(block=FAKE, ldb=64, block_dtype=0, scale=1.0, post_eps=1e-6)
+    assert L.mobi_norm(None, None) == 1
+    assert call(T=0) == 0 and call(T=0, **blk) == 0
+    assert call(T=-1) == 1 and call(D=0) == 1 and call(D=16385, ldx=16385, ldn=16385) == 2 and call(T=1 << 29) == 2
+    assert call(x=None) == 1 and call(n_out=None) == 1 and call(out_dtype=3) == 1  # no scales
+    assert call(x_dtype=3) == 1 and call(out_dtype=4) == 1 and call(kind=3) == 1 and call(kind=-1) == 1
+    assert call(eps=-1.0) == 1 and call(eps=float("nan")) == 1 and call(eps=float("inf")) == 1
+    assert call(ldx=63) == 1 and call(ldn=63) == 1
+    assert call(weight=FAKE, weight_dtype=3) == 1
+    assert call(**{**blk, "ldb": 63}) == 1 and call(**{**blk, "block_dtype": 3}) == 1
+    assert call(**{**blk, "scale": float("nan")}) == 1 and call(**{**blk, "post_eps": -1.0}) == 1
+    assert call(gate=FAKE, gate_dtype=3, **blk) == 1 and call(post=3, **blk) == 1
+    assert call(r_out=FAKE, ldr=63, **blk) == 1
+    assert call(r_out=FAKE, ldr=72, ldx=64, **blk) == 1  # in place with another pitch
+    assert call(x=FAKE + 1) == 3 and call(weight=FAKE + 1, weight_dtype=1) == 3 and call(n_out=FAKE + 1) == 3
+    assert call(gate=FAKE + 2, gate_dtype=0, **blk) == 3 and call(r_out=FAKE + 1, ldr=64, **blk) == 3
+
+
+def test_logprobs_refusals(L):
+    def call(x=FAKE, dt=0, T=4, V=100, ld=100, tg=FAKE, temp=1.0, k=5, lp=FAKE, en=FAKE, tl=FAKE, ti=FAKE):
+        return L.mobi_logprobs(x, dt, T, V, ld, tg, temp, k, lp, en, tl, ti, None)
+    assert call(T=0) == 0
+    assert call(T=-1) == 1 and call(V=0) == 1 and call(dt=3) == 1 and call(k=-1) == 1 and call(k=33) == 1
+    assert call(V=1 << 29, ld=1 << 29) == 2
+    for t in (0.0, -1.0, float("nan"), float("inf"), 1e-31):
+        assert call(temp=t) == 1, t
+    assert call(x=None) == 1 and call(ld=99) == 1 and call(lp=None) == 1
+    assert call(tl=None) == 1 and call(ti=None) == 1
+    assert call(x=FAKE + 2) == 3 and call(dt=1, x=FAKE + 1) == 3 and call(tg=FAKE + 4) == 3 and call(ti=FAKE + 2) == 3
+
+
+def test_binding_takes_cuda_tensors_only():
+    x = torch.zeros(4, 128)
+    q, s = x.to(torch.float8_e4m3fn), torch.ones(1, 4)
+    for f in (lambda: mobi.mobi_fp8_quant(x), lambda: mobi.mobi_fp8_gemm(q, s, q, s),
+              lambda: mobi.mobi_fp8_gated(q, s, q, s, q, s), lambda: mobi.mobi_norm(x),
+              lambda: mobi.mobi_logprobs(x)):
+        with pytest.raises(ValueError):
+            f()
+
+
+def test_reference_quantiser():
+    """The tests' own quantiser against hand-made values: the scale, ties to even, the floor of the scale, a NaN."""
+    import block_ref as ref
+    x = torch.zeros(2, 128)
+    x[0, 0], x[0, 1], x[0, 2], x[0, 3] = 448.0, 17.0, 19.0, -0.0009765625  # 17: between 16 and 18; 2^-10: half of 2^-9
+    x[1, 5] = float("nan")
+    q, s = ref.quant(x, 1)
+    assert s[0, 0] == 1.0 and torch.isnan(s[0, 1])
+    assert q[0, :4].float().tolist() == [448.0, 16.0, 20.0, 0.0]
+    assert torch.isnan(q[1].float()).all()
+    q, s = ref.quant(torch.zeros(1, 5), 1)
+    assert s[0, 0] == 2.0 ** -126 and (q.float() == 0).all()
+
+
+def test_reference_logprobs():
+    """The tests' own scoring against torch's."""
+    import block_ref as ref
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(3, 50, generator=g) * 3
+    x[1, 7] = float("-inf")
+    t = torch.tensor([4, 7, -1])
+    lp, H, top, idx, _, _ = ref.logprobs(x, t, 0.7, 4)
+    want = torch.log_softmax(x.double() / 0.7, 1)
+    assert torch.allclose(lp[:1], want[:1, 4]) and lp[1] == float("-inf") and lp[2] == 0
+    p = want.exp()
+    assert torch.allclose(H, -torch.xlogy(p, p).sum(1))
+    assert torch.equal(idx, x.topk(4, 1)[1])
+    assert torch.allclose(top, want.gather(1, idx))

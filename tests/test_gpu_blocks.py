@@ -1,0 +1,538 @@
+"""The 8-bit layer, the norm between blocks and the scoring of logits against
+their plain 64-bit forms (block_ref.py has the forms and the bounds)."""
+import math
+
+import pytest
+import torch
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E4M3 = torch.float8_e4m3fn
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def mobi():
+    import token_adaptive_mixed_b200 as m
+    from token_adaptive_mixed_b200 import build
+    build.build()
+    m.lib()
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def same_codes(q, want):
+    return torch.equal(q.contiguous().view(torch.uint8).cpu(), want.contiguous().view(torch.uint8))
+
+
+# ---- quantiser: bit-exact ---------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("T,K", [(1, 128), (1, 1), (3, 100), (17, 512), (130, 300), (257, 1037), (128, 4096)])
+def test_quant(mobi, T, K, rows, dtype):
+    g = gen(T * 10007 + K)
+    x = (torch.randn(T, K, generator=g) * torch.exp(torch.randn(T, 1, generator=g) * 3)).clamp(-6e4, 6e4).to(dtype)
+    q, s = mobi.mobi_fp8_quant(x.to(DEV), block_rows=rows)
+    wq, ws = ref.quant(x, rows)
+    assert torch.equal(s.cpu(), ws) and same_codes(q, wq)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quant_edges(mobi, rows):
+    """Zero blocks, the scale's floor, the largest values, infinities and NaN; rows that are a slice of others."""
+    x = torch.randn(256, 640, generator=gen(1))
+    x[:, :128] = 0
+    x[:128, 128:256] *= 1e-42
+    x[3, 256] = float("nan")
+    x[200, 300] = float("inf")
+    x[:, 400] = 3.4e38
+    x[5, 639] = -0.0
+    q, s = mobi.mobi_fp8_quant(x.to(DEV), block_rows=rows)
+    wq, ws = ref.quant(x, rows)
+    assert torch.equal(s.cpu().view(torch.int32)[~torch.isnan(ws)], ws.view(torch.int32)[~torch.isnan(ws)])
+    assert torch.equal(torch.isnan(s.cpu()), torch.isnan(ws))
+    a, b = q.float().cpu(), wq.float()
+    assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a[~torch.isnan(b)], b[~torch.isnan(b)])
+    big = x.to(DEV)
+    for part in (big[:, 3:500], big[1:, 8:], big[::3, 16:400]):
+        q, s = mobi.mobi_fp8_quant(part, block_rows=rows)
+        wq, ws = ref.quant(part.cpu(), rows)
+        assert torch.equal(torch.nan_to_num(s.cpu()), torch.nan_to_num(ws))
+        assert torch.equal(torch.nan_to_num(q.float().cpu()), torch.nan_to_num(wq.float()))
+
+
+# ---- products -------------------------------------------------------------------------------
+
+# Both kernels, every token tile, every split of K (one block to eight CTAs), ragged K, odd N and T.
+GEMM = [(1, 128, 128), (1, 1, 16), (1, 4096, 4096), (2, 300, 1000), (16, 129, 2048), (17, 640, 272), (32, 77, 1536),
+        (33, 500, 640), (64, 1024, 512), (65, 200, 128), (128, 257, 1040), (129, 384, 3200), (200, 4096, 1024),
+        (256, 256, 128), (333, 4099, 512), (1000, 1500, 384), (2049, 513, 272), (37, 9000, 144), (100, 16, 8192)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,N,K", GEMM)
+def test_gemm(mobi, T, N, K, dtype):
+    g = gen(T + 1009 * N + K)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, 0.02, device=DEV)
+    x, w = _pitched(x), _pitched(w)
+    buf = torch.full((T + 2, N + 8), 7.0, dtype=dtype, device=DEV)
+    y = mobi.mobi_fp8_gemm(x, xs, w, ws, out_dtype=dtype, Y=buf[1:T + 1, 3:N + 3])
+    mobi.mobi_sync_check()
+    want, err = ref.product(x, xs, w, ws)
+    ref.check_close(y, want, ref.rounded(want, err, dtype), f"{T}x{N}x{K}")
+    buf[1:T + 1, 3:N + 3] = 7.0
+    assert (buf == 7.0).all(), "written outside Y"
+
+
+def _pitched(q):
+    """The same codes with rows 16 bytes apart or more (K need not be a multiple of 16)."""
+    R, K = q.shape
+    p = torch.empty((R, (K + 15) // 16 * 16 + 16), dtype=E4M3, device=q.device)
+    p.view(torch.uint8).fill_(0x7f)  # NaN codes beside the rows: they must not be read as values
+    p[:, :K] = q
+    return p[:, :K]
+
+
+@pytest.mark.parametrize("K", [1, 15, 129, 250])
+def test_gemm_any_k(mobi, K):
+    for T, N in ((5, 40), (300, 300)):
+        g = gen(K)
+        x, xs = ref.operand(T, K, 1, g, device=DEV)
+        w, ws = ref.operand(N, K, 128, g, device=DEV)
+        x, w = _pitched(x), _pitched(w)
+        want, err = ref.product(x, xs, w, ws)
+        ref.check_close(mobi.mobi_fp8_gemm(x, xs, w, ws), want, ref.rounded(want, err, F32))
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_gemm_single_blocks(mobi, T):
+    """One block at a time has to count, with its own scales: the others' codes are zero."""
+    N, K = 384, 640
+    g = gen(T)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, device=DEV)
+    for b in range(5):
+        xb = torch.zeros_like(x)
+        xb[:, 128 * b:128 * b + 128] = x[:, 128 * b:128 * b + 128]
+        want, err = ref.product(xb, xs, w, ws)
+        assert want.abs().max() > 0
+        ref.check_close(mobi.mobi_fp8_gemm(xb, xs, w, ws), want, ref.rounded(want, err, F32))
+
+
+@pytest.mark.parametrize("T", [9, 400])
+def test_gemm_nan_stays_in_its_row(mobi, T):
+    N, K = 300, 512
+    g = gen(5)
+    x = torch.randn(T, K, generator=g)
+    x[2, 200] = float("nan")
+    x[4, 10] = float("inf")
+    q, s = mobi.mobi_fp8_quant(x.to(DEV))
+    w, ws = ref.operand(N, K, 128, g, device=DEV)
+    y = mobi.mobi_fp8_gemm(q, s, w, ws)
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[2] = bad[4] = True
+    assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all()
+    h, hs = mobi.mobi_fp8_gated(q, s, w, ws, w, ws, out_dtype=E4M3)
+    assert torch.isnan(h.float()[bad]).all() and torch.isfinite(h.float()[~bad]).all()
+    assert torch.isnan(hs[:, bad]).all() and torch.isfinite(hs[:, ~bad]).all()
+
+
+GATED = [(1, 128, 128), (1, 16, 48), (7, 144, 272), (8, 2048, 1024), (16, 100, 2048), (20, 640, 512), (32, 1000, 272),
+         (33, 300, 640), (64, 200, 1024), (130, 129, 256), (200, 4096, 512), (300, 1000, 400), (1030, 700, 256)]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("T,N,K", GATED)
+def test_gated(mobi, T, N, K, act):
+    g = gen(T + 7 * N + K)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    wg, gs = ref.operand(N, K, 128, g, 0.05, device=DEV)
+    wu, us = ref.operand(N, K, 128, g, 0.05, device=DEV)
+    h, err = ref.gated(x, xs, wg, gs, wu, us, act)
+    for dtype in (F32, BF16, F16):
+        y = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, act=act, out_dtype=dtype)
+        ref.check_close(y, h, ref.rounded(h, err, dtype), f"{dtype}")
+    buf = torch.full((T + 2, (N + 15) // 16 * 16 + 16), 3.0, device=DEV).to(E4M3)
+    q, s = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, act=act, out_dtype=E4M3, H=buf[1:T + 1, :N])
+    mobi.mobi_sync_check()
+    ref.check_quantised(q, s, h, err)
+    buf.view(torch.uint8)[1:T + 1, :N] = torch.full((1,), 3.0).to(E4M3).view(torch.uint8).to(DEV)
+    assert (buf.float() == 3.0).all(), "written outside H"
+
+
+def test_products_do_not_depend_on_timing(mobi):
+    """The same call gives the same bits, alone and beside another on a second stream."""
+    g = gen(3)
+    x, xs = ref.operand(48, 4096, 1, g, device=DEV)
+    w, ws = ref.operand(2000, 4096, 128, g, device=DEV)
+    u, us = ref.operand(2000, 4096, 128, g, device=DEV)
+    first = mobi.mobi_fp8_gemm(x, xs, w, ws)
+    gat = mobi.mobi_fp8_gated(x, xs, w, ws, u, us)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(10):
+        with torch.cuda.stream(a):
+            y = mobi.mobi_fp8_gemm(x, xs, w, ws)
+        h = mobi.mobi_fp8_gated(x, xs, w, ws, u, us, stream=b)
+        outs.append((y, h))
+    torch.cuda.synchronize()
+    mobi.mobi_sync_check()
+    assert all(torch.equal(y, first) and torch.equal(h, gat) for y, h in outs)
+
+
+@pytest.mark.parametrize("T", [8, 64, 600])
+def test_product_timeout_is_reported(mobi, T):
+    """A wait that runs out ends the kernel with an error status; the next call is right again."""
+    N, K = 1024, 4096
+    g = gen(T)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, device=DEV)
+    u, us = ref.operand(N, K, 128, g, device=DEV)
+    for call in (lambda: mobi.mobi_fp8_gemm(x, xs, w, ws),
+                 lambda: mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3)[0]):
+        good = call()
+        mobi.mobi_sync_check()
+        mobi.mobi_debug_set_wait_limit(1)
+        try:
+            call()
+            with pytest.raises(mobi.MobiError) as e:
+                mobi.mobi_sync_check()
+            assert e.value.status == 6  # MOBI_ERR_TIMEOUT
+        finally:
+            mobi.mobi_debug_set_wait_limit(0)
+        again = call()
+        mobi.mobi_sync_check()
+        assert torch.equal(again.view(torch.uint8), good.view(torch.uint8))
+
+
+# ---- norm -----------------------------------------------------------------------------------
+
+
+def norm_case(T, D, xd, bd, wd, gate, post, kind, g, out):
+    x = torch.randn(T, D, generator=g) * 3 + 0.5
+    b = torch.randn(T, D, generator=g) * 0.7 - 0.2
+    vec = lambda s: (1.0 + torch.randn(D, generator=g) * s).to(wd).to(DEV)  # noqa: E731
+    shape = {"none": None, "channel": (D,), "token": (T, 1), "full": (T, D), "one": (1,)}[gate]
+    return dict(x=x.to(xd).to(DEV), weight=vec(0.1), bias=vec(0.2) if kind == "layer" else None, eps=1e-5, kind=kind,
+                block=b.to(bd).to(DEV) if bd is not None else None,
+                **(dict(post=post, post_weight=vec(0.1) if post != "none" else None,
+                        post_bias=vec(0.3) if post == "layer" else None, post_eps=1e-4,
+                        gate=(torch.randn(*shape, generator=g)).to(F16 if gate == "token" else BF16).to(DEV)
+                        if shape else None, scale=0.7) if bd is not None else {}))
+
+
+def check_norm(mobi, case, out, **more):
+    got = mobi.mobi_norm(out_dtype=out, **case, **more)
+    mobi.mobi_sync_check()
+    n, en, r, er = ref.norm(**case)
+    if case["block"] is not None:
+        got, rr = got
+        ref.check_close(rr, r, ref.rounded(r, er, rr.dtype), "r")
+    if out is E4M3:
+        ref.check_quantised(got[0], got[1], n, en, "n")
+    else:
+        ref.check_close(got, n, ref.rounded(n, en, out), "n")
+
+
+@pytest.mark.parametrize("D", [1, 7, 8, 100, 128, 250, 512, 1000, 4096, 4097, 5000, 8192, 11008, 16384])
+@pytest.mark.parametrize("T,kind,post,gate,out", [
+    (1, "rms", "none", "none", BF16), (5, "layer", "rms", "channel", F32), (3, "rms", "layer", "token", E4M3),
+    (9, "layer", "none", "full", F16), (2, "none", "rms", "one", F32)])
+def test_norm(mobi, T, D, kind, post, gate, out):
+    g = gen(T * 31 + D)
+    for xd, bd, wd in ((BF16, F32, BF16), (F32, BF16, F32), (F16, F16, F16)):
+        check_norm(mobi, norm_case(T, D, xd, bd, wd, gate, post, kind, g, out), out)
+
+
+@pytest.mark.parametrize("T,D", [(1, 4096), (700, 512), (2000, 4096), (1200, 96), (800, 6000), (650, 77), (600, 16384)])
+def test_norm_many_rows(mobi, T, D):
+    g = gen(D)
+    check_norm(mobi, norm_case(T, D, BF16, BF16, BF16, "channel", "rms", "rms", g, E4M3), E4M3)
+    check_norm(mobi, norm_case(T, D, F32, F32, F32, "full", "layer", "layer", g, F32), F32)
+    check_norm(mobi, norm_case(T, D, BF16, None, BF16, "none", "none", "rms", g, BF16), BF16)
+
+
+@pytest.mark.parametrize("D", [264, 265])
+def test_norm_slices_in_place_and_offset(mobi, D):
+    """Rows of larger tensors, the residual stream updated in place, weights counted as 1 + w, no weights at all."""
+    g = gen(D)
+    T = 40
+    big = torch.randn(T, D + 32, generator=g).to(BF16).to(DEV)
+    for off in (0, 8, 3):
+        x = big.clone()[:, off:off + D]
+        keep = x.clone()
+        blk = torch.randn(T, D + 16, generator=g).to(DEV)[:, 8:8 + D]
+        w = (torch.randn(D, generator=g) * 0.1).to(DEV)
+        n, en, r, er = ref.norm(keep, w, None, 1e-6, "rms", block=blk, scale=1.0, unit_offset=True)
+        y, rr = mobi.mobi_norm(x, w, block=blk, unit_offset=True, R=x)
+        assert rr.data_ptr() == x.data_ptr()
+        ref.check_close(x, r, ref.rounded(r, er, BF16), "r")
+        ref.check_close(y, n, ref.rounded(n, en, BF16), "n")
+        n, en, _, _ = ref.norm(keep, None, None, 1e-6, "layer")
+        out = torch.full((T, D + 9), 5.0, device=DEV)
+        mobi.mobi_norm(keep, kind="layer", out_dtype=F32, N=out[:, 4:4 + D])
+        ref.check_close(out[:, 4:4 + D], n, ref.rounded(n, en, F32), "plain")
+        assert (out[:, :4] == 5.0).all() and (out[:, 4 + D:] == 5.0).all()
+
+
+def test_norm_special_rows(mobi):
+    """A zero row, rows with an infinity or a NaN, constant rows: the others are untouched by them."""
+    T, D = 6, 520
+    x = torch.randn(T, D, generator=gen(9))
+    x[0] = 0
+    x[1, 5] = float("inf")
+    x[2, 7] = float("nan")
+    x[3] = 2.5
+    for kind in ("rms", "layer"):
+        for out in (F32, E4M3):
+            y = mobi.mobi_norm(x.to(DEV), kind=kind, out_dtype=out, eps=1e-6)
+            v = (y[0] if out is E4M3 else y).float()
+            n, en, _, _ = ref.norm(x.to(DEV), None, None, 1e-6, kind)
+            assert (v[0] == 0).all() and torch.isnan(v[2]).any()
+            if out is F32:
+                ref.check_close(v[4:], n[4:], ref.rounded(n, en, F32)[4:])
+                ref.check_close(v[3], n[3], ref.rounded(n, en, F32)[3])
+
+
+# ---- scoring --------------------------------------------------------------------------------
+
+
+def check_scores(mobi, x, targets, temp, k):
+    lp, H, top, idx = mobi.mobi_logprobs(x, targets, temperature=temp, top_k=k)
+    wl, wH, wt, wi, elog, eH = ref.logprobs(x, targets, temp, k)
+    assert torch.equal(idx, wi.to(torch.int32)), "alternatives"
+
+    def close(got, want, bound, what):
+        inf = torch.isneginf(want)
+        assert torch.equal(torch.isneginf(got), inf), what
+        z = torch.zeros_like(want)
+        ref.check_close(torch.where(inf, z.float(), got), torch.where(inf, z, want),
+                        torch.where(inf, z, bound) + 1e-300, what)
+    # (x - m) / t: a rounding each, and the difference from ln S.
+    if targets is not None:
+        ignored = targets < 0
+        assert (lp[ignored] == 0).all()
+        close(lp, wl, elog[:, 0] + 6 * ref.U * wl.abs() + 3 * ref.U * elog[:, 0], "log probability")
+    else:
+        assert lp is None
+    close(H, wH, eH, "entropy")
+    close(top, wt, elog + 6 * ref.U * wt.abs(), "top")
+
+
+SHAPES = [(1, 1), (2, 7), (3, 33), (5, 1000), (4, 4099), (2, 32000), (1, 131073), (150, 5000), (300, 700)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,V", SHAPES)
+def test_logprobs(mobi, T, V, dtype):
+    g = gen(T * 7 + V)
+    x = (torch.randn(T, V, generator=g) * 3).to(dtype).to(DEV)
+    t = torch.randint(-1, V, (T,), generator=g).to(DEV)
+    for temp, k in ((1.0, 5), (0.6, 0), (3.0, 20), (1.0, 32)):
+        check_scores(mobi, x, t, temp, k)
+    check_scores(mobi, x, None, 1.0, 1)
+    mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,V", [(2, 7), (3, 1000), (4, 32000), (2, 131073), (200, 3000)])
+@pytest.mark.parametrize("mask", ["some", "few", "empty", "ties", "constant", "rounded"])
+def test_logprobs_masks_and_ties(mobi, T, V, dtype, mask):
+    """Masked entries, rows with fewer left than asked for, rows with nothing left, equal entries (the lowest index)."""
+    g = gen(V)
+    x = torch.randn(T, V, generator=g) * 2
+    drop = torch.rand(T, V, generator=g)
+    if mask == "some":
+        x[drop < 0.5] = float("-inf")
+    elif mask == "few":
+        x[drop > 4.0 / V] = float("-inf")
+    elif mask == "empty":
+        x[T // 2] = float("-inf")
+    elif mask == "ties":
+        x = torch.where(drop < 0.01, 5.0, torch.where(drop < 0.5, 4.0, -1.0))
+    elif mask == "constant":
+        x[:] = -2.5
+    else:
+        x = x.round()
+    t = torch.randint(0, V, (T,), generator=g).to(DEV)
+    for k in (1, 20, 32):
+        check_scores(mobi, x.to(dtype).to(DEV), t, 0.9, k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,V", [(3, 1000), (2, 40000), (160, 2000)])
+def test_logprobs_lowest_value_masks(mobi, T, V, dtype):
+    """A mask of the type's lowest value: those entries are finite, so they stand behind the rest by index, with a
+    probability of 0 beside any other and of 1/n among themselves."""
+    g = gen(V + 1)
+    low = torch.finfo(dtype).min
+    x = torch.randn(T, V, generator=g) * 2
+    x[torch.rand(T, V, generator=g) > 8.0 / V] = low
+    x[0] = low
+    x[1, ::2] = float("-inf")
+    x[1, 1::2] = low
+    x = x.clamp_min(low).to(dtype) if dtype != F16 else x.to(dtype)
+    x[1, ::2] = float("-inf")
+    d = x.to(DEV)
+    for k in (0, 5, 32):
+        lp, H, top, idx = mobi.mobi_logprobs(d, torch.full((T,), 1, device=DEV), temperature=1.3, top_k=k)
+        order = torch.argsort(-d.double(), dim=1, stable=True)[:, :k]
+        assert torch.equal(idx, order.to(torch.int32))
+        n = [V, V // 2]
+        for row in (0, 1):
+            tol = (V / 256 + 40) * ref.U * 16 + 8 * ref.U * math.log(V)
+            assert abs(lp[row].item() + math.log(n[row])) <= tol and abs(H[row].item() - math.log(n[row])) <= 2 * tol
+            if k:
+                assert (top[row].double() + math.log(n[row])).abs().max().item() <= tol
+
+
+def test_logprobs_extremes(mobi):
+    """Large logits and temperatures, an infinity, a NaN, a target outside the vocabulary, rows of a larger tensor."""
+    g = gen(4)
+    x = torch.randn(6, 500, generator=g)
+    x[1] *= 1e30
+    x[2] *= 1e-30
+    for temp in (1e-3, 1.0, 1e6):
+        check_scores(mobi, x[[0, 2, 3]].to(DEV), torch.tensor([3, 4, 5], device=DEV), temp, 8)
+    lp, H, top, idx = mobi.mobi_logprobs(x[1:2].to(DEV), torch.tensor([7], device=DEV), top_k=1)
+    best = int(x[1].argmax())
+    assert idx[0, 0] == best and top[0, 0] == 0 and H[0] == 0
+    y = x.clone()
+    y[0, 3] = float("nan")
+    y[4, 9] = float("inf")
+    lp, H, top, idx = mobi.mobi_logprobs(y.to(DEV), torch.zeros(6, dtype=torch.int64, device=DEV), top_k=3)
+    assert torch.isnan(lp[[0, 4]]).all() and torch.isnan(H[[0, 4]]).all() and torch.isfinite(lp[[2, 3, 5]]).all()
+    mobi.mobi_sync_check()
+    lp, _, _, _ = mobi.mobi_logprobs(x.to(DEV), torch.tensor([0, 0, 0, 500, 0, 0], device=DEV))
+    assert torch.isnan(lp[3]) and torch.isfinite(lp[[0, 2, 4, 5]]).all()
+    with pytest.raises(mobi.MobiError) as e:
+        mobi.mobi_sync_check()
+    assert e.value.status == 1
+    mobi.mobi_sync_check()
+    big = torch.randn(9, 1100, generator=g).to(BF16).to(DEV)
+    for part in (big[:, 1:1000], big[::2, 8:900], big[:, 3:4]):
+        check_scores(mobi, part, torch.zeros(part.shape[0], dtype=torch.int64, device=DEV), 1.0, 4)
+
+
+# ---- together -------------------------------------------------------------------------------
+
+
+def test_empty_calls(mobi):
+    z = lambda *s, dtype=F32: torch.empty(*s, dtype=dtype, device=DEV)  # noqa: E731
+    q, s = mobi.mobi_fp8_quant(z(0, 256))
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+    w, ws = mobi.mobi_fp8_quant(torch.ones(64, 256, device=DEV), block_rows=128)
+    assert mobi.mobi_fp8_gemm(q, s, w, ws).shape == (0, 64)
+    h, hs = mobi.mobi_fp8_gated(q, s, w, ws, w, ws, out_dtype=E4M3)
+    assert h.shape == (0, 64) and hs.shape == (1, 0)
+    assert mobi.mobi_norm(z(0, 256)).shape == (0, 256)
+    lp, H, top, idx = mobi.mobi_logprobs(z(0, 100), z(0, dtype=torch.int64), top_k=3)
+    assert lp.shape == (0,) and top.shape == (0, 3)
+    mobi.mobi_sync_check()
+
+
+def test_refusals_of_the_binding(mobi):
+    x = torch.randn(4, 256, device=DEV)
+    q, s = mobi.mobi_fp8_quant(x)
+    w, ws = mobi.mobi_fp8_quant(x, block_rows=128)
+    bad = [lambda: mobi.mobi_fp8_quant(x, block_rows=64), lambda: mobi.mobi_fp8_quant(x.t()),
+           lambda: mobi.mobi_fp8_quant(x.double()), lambda: mobi.mobi_fp8_quant(x[0]),
+           lambda: mobi.mobi_fp8_gemm(q, s, w, s), lambda: mobi.mobi_fp8_gemm(q, s, w[:, :128], ws),
+           lambda: mobi.mobi_fp8_gemm(q.float(), s, w, ws), lambda: mobi.mobi_fp8_gemm(q, s, w, ws, out_dtype=E4M3),
+           lambda: mobi.mobi_fp8_gemm(q, s, w, ws, Y=torch.empty(4, 5, device=DEV)),
+           lambda: mobi.mobi_fp8_gated(q, s, w, ws, w[:2], ws), lambda: mobi.mobi_fp8_gated(q, s, w, ws, w, ws, act="x"),
+           lambda: mobi.mobi_norm(x, torch.ones(255, device=DEV)), lambda: mobi.mobi_norm(x, kind="group"),
+           lambda: mobi.mobi_norm(x, block=x[:2]), lambda: mobi.mobi_norm(x, gate=x),
+           lambda: mobi.mobi_norm(x, torch.ones(256, device=DEV), torch.ones(256, device=DEV).half()),
+           lambda: mobi.mobi_norm(x, block=x, gate=torch.ones(3, 1, device=DEV)),
+           lambda: mobi.mobi_logprobs(x, torch.zeros(4, dtype=torch.int32, device=DEV)),
+           lambda: mobi.mobi_logprobs(x, top_k=33), lambda: mobi.mobi_logprobs(x, temperature=0.0)]
+    for f in bad:
+        with pytest.raises((ValueError, RuntimeError)):
+            f()
+    mobi.mobi_sync_check()
+
+
+def _layer(mobi, T, seed):
+    """A block's feed-forward half and the head, as a user would chain them; returns a function of (x, y) and its parts."""
+    D, F, V = 256, 640, 1000
+    g = gen(seed)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(DEV)  # noqa: E731
+    ws = {k: mobi.mobi_fp8_quant(rnd(n, m, std=0.06), block_rows=128) for k, n, m in
+          (("g", F, D), ("u", F, D), ("d", D, F))}
+    head, sz = mobi.mobi_pack(rnd(((V + 15) // 16) * 16, D, std=0.1).half())
+    wr = rnd(D, 3, std=0.05)
+    w1, w2 = (1 + rnd(D, std=0.1)).bfloat16(), (1 + rnd(D, std=0.1)).bfloat16()
+    gate = rnd(D, std=0.5).bfloat16()
+
+    def run(x, y, targets):
+        (n, ns), r = mobi.mobi_norm(x, w1, block=y, post="rms", post_weight=w2, gate=gate, scale=0.5, out_dtype=E4M3)
+        h, hs = mobi.mobi_fp8_gated(n, ns, *ws["g"], *ws["u"], out_dtype=E4M3)
+        d = mobi.mobi_fp8_gemm(h, hs, *ws["d"])
+        f, r2 = mobi.mobi_norm(r, w2, block=d)
+        logits, k_t, _, _ = mobi.mobi_linear(f, wr, None, head, sz, ((V + 15) // 16) * 16)
+        return (n, ns, r, h, hs, d, f, r2, logits, k_t) + mobi.mobi_logprobs(logits[:, :V], targets, top_k=5)
+    return run, ws, (w1, w2, gate), rnd, V
+
+
+@pytest.mark.parametrize("T", [1, 12, 100, 500])
+def test_run_together(mobi, T):
+    """Norm -> gated product -> down projection -> norm -> mixed-bit head -> scoring, each step against its plain form
+    on the inputs that it got."""
+    run, ws, (w1, w2, gate), rnd, V = _layer(mobi, T, 11)
+    x, y = rnd(T, 256).bfloat16(), rnd(T, 256)
+    t = torch.randint(0, V, (T,), generator=gen(T)).to(DEV)
+    n, ns, r, h, hs, d, f, r2, logits, k_t, lp, H, top, idx = run(x, y, t)
+    mobi.mobi_sync_check()
+    wn, en, wr_, er = ref.norm(x, w1, None, 1e-6, "rms", block=y, post="rms", post_weight=w2, gate=gate, scale=0.5)
+    ref.check_close(r, wr_, ref.rounded(wr_, er, BF16), "r")
+    ref.check_quantised(n, ns, wn, en, "n")
+    wh, eh = ref.gated(n, ns, *ws["g"], *ws["u"], "silu")
+    ref.check_quantised(h, hs, wh, eh, "h")
+    wd, ed = ref.product(h, hs, *ws["d"])
+    ref.check_close(d, wd, ref.rounded(wd, ed, F32), "d")
+    wf, ef, w2r, e2r = ref.norm(r, w2, None, 1e-6, "rms", block=d)
+    ref.check_close(f, wf, ref.rounded(wf, ef, BF16), "f")
+    ref.check_close(r2, w2r, ref.rounded(w2r, e2r, BF16), "r2")
+    wl, wH, wt, wi, elog, eH = ref.logprobs(logits[:, :V], t, 1.0, 5)
+    assert torch.equal(idx, wi.to(torch.int32))
+    ref.check_close(lp, wl, elog[:, 0] + 6 * ref.U * wl.abs(), "lp")
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_captured_and_replayed(mobi, T):
+    """The chain captured into two graphs that are replayed in turn with new inputs gives what eager calls give."""
+    run, _, _, rnd, V = _layer(mobi, T, 12)
+    bufs = [(rnd(T, 256).bfloat16(), rnd(T, 256), torch.randint(0, V, (T,), generator=gen(i)).to(DEV)) for i in range(2)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for b in bufs:
+            run(*b)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for b in bufs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(run(*b))
+        graphs.append(gr)
+    for rep in range(3):
+        for b in bufs:
+            b[0].copy_(rnd(T, 256))
+            b[1].copy_(rnd(T, 256))
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        mobi.mobi_sync_check()
+        got = [[o.clone() for o in out] for out in outs]
+        for b, out in zip(bufs, got):
+            for a, e in zip(out, run(*b)):
+                assert torch.equal(a.contiguous().view(torch.uint8), e.contiguous().view(torch.uint8))
