@@ -110,21 +110,25 @@ def _scales(s: torch.Tensor, kb: int, rb: int, what: str, device) -> int:
     return s.data_ptr()
 
 
-def _out(t, shape, dtype, what, device, dev):
-    """A given output checked, or a new one."""
+def _out(t, T: int, N: int, dtype, what, device, dev):
+    """(output, its row pitch): a given one checked, or a new one. Rows of a new e4m3 output start at multiples of
+    16 bytes, as the products take them. (Sizes are passed to torch.empty one by one: a tuple costs another 0.7 us.)"""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _on(t, what, device)
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
-    return t
+        if dtype is E4M3 and N & 15:
+            ld = (N + 15) & ~15
+            return torch.empty(T, ld, dtype=E4M3, device=dev)[:, :N], ld
+        return torch.empty(T, N, dtype=dtype, device=dev), N
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != T or t.shape[1] != N:
+        raise ValueError(f"{what} must be {dtype} of shape ({T}, {N})")
+    return t, _matrix(t, what, device)[2]
 
 
-def _codes(T: int, K: int, dev) -> torch.Tensor:
-    """A new e4m3 [T, K] whose rows start at multiples of 16 bytes."""
-    ld = (K + 15) & ~15
-    q = torch.empty((T, ld), dtype=E4M3, device=dev)
-    return q if ld == K else q[:, :K]
+def _new_scales(t, kb: int, rb: int, what, device, dev):
+    """(scales, their address): given ones checked, or new ones."""
+    if t is None:
+        t = torch.empty(kb, rb, dtype=torch.float32, device=dev)
+        return t, t.data_ptr()
+    return t, _scales(t, kb, rb, what, device)
 
 
 def mobi_fp8_quant(X: torch.Tensor, block_rows: int = 1, Q: torch.Tensor | None = None,
@@ -139,12 +143,9 @@ def mobi_fp8_quant(X: torch.Tensor, block_rows: int = 1, Q: torch.Tensor | None 
         raise ValueError("block_rows must be 1 or 128")
     d, dev = X.get_device(), X.device
     kb, rb = (K + 127) >> 7, T if block_rows == 1 else (T + 127) >> 7
-    Q = _codes(T, K, dev) if Q is None else _out(Q, (T, K), E4M3, "Q", d, dev)
-    if scale is None:
-        scale = torch.empty((kb, rb), dtype=torch.float32, device=dev)
-    sp = _scales(scale, kb, rb, "scale", d)
-    _call("mobi_fp8_quant", d, stream, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), _matrix(Q, "Q", d)[2],
-          sp)
+    Q, ldq = _out(Q, T, K, E4M3, "Q", d, dev)
+    scale, sp = _new_scales(scale, kb, rb, "scale", d, dev)
+    _call("mobi_fp8_quant", d, stream, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), ldq, sp)
     return Q, scale
 
 
@@ -171,8 +172,8 @@ def mobi_fp8_gemm(X: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, ws: torch.
     dt = _DT.get(out_dtype, 3)
     if dt == 3:
         raise ValueError("out_dtype must be fp32, bf16 or fp16")
-    Y = _out(Y, (T, N), out_dtype, "Y", d, X.device)
-    _call("mobi_fp8_gemm", d, stream, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), _matrix(Y, "Y", d)[2])
+    Y, ldy = _out(Y, T, N, out_dtype, "Y", d, X.device)
+    _call("mobi_fp8_gemm", d, stream, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), ldy)
     return Y
 
 
@@ -193,16 +194,12 @@ def mobi_fp8_gated(X: torch.Tensor, xs: torch.Tensor, Wg: torch.Tensor, gs: torc
     dt = _DT.get(out_dtype)
     if dt is None:
         raise ValueError("out_dtype must be fp32, bf16, fp16 or e4m3")
+    H, ldh = _out(H, T, N, out_dtype, "H", d, dev)
     hsp = None
     if dt == 3:
-        H = _codes(T, N, dev) if H is None else _out(H, (T, N), E4M3, "H", d, dev)
-        if hs is None:
-            hs = torch.empty(((N + 127) >> 7, T), dtype=torch.float32, device=dev)
-        hsp = _scales(hs, (N + 127) >> 7, T, "hs", d)
-    else:
-        H = _out(H, (T, N), out_dtype, "H", d, dev)
+        hs, hsp = _new_scales(hs, (N + 127) >> 7, T, "hs", d, dev)
     _call("mobi_fp8_gated", d, stream, xp, ldx, xsp, T, K, gp, ldg, gsp, up, ldu, usp, N, _ACT[act], dt, H.data_ptr(),
-          _matrix(H, "H", d)[2], hsp)
+          ldh, hsp)
     return (H, hs) if dt == 3 else H
 
 
@@ -254,18 +251,14 @@ def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
                 raise ValueError("gate must be fp32, bf16 or fp16")
             a.gate_st, a.gate_sd = gate.expand(T, D).stride()
             a.gate = gate.data_ptr()
-        R = _out(R, (T, D), x.dtype, "R", d, dev)
-        a.r_out, a.ldr = R.data_ptr(), _matrix(R, "R", d)[2]
+        R, a.ldr = _out(R, T, D, x.dtype, "R", d, dev)
+        a.r_out = R.data_ptr()
     elif R is not None or gate is not None or post_weight is not None or post_bias is not None:
         raise ValueError("R, gate and the post norm's weights need a block")
+    N, a.ldn = _out(N, T, D, out_dtype, "N", d, dev)
+    a.n_out = N.data_ptr()
     if odt == 3:
-        N = _codes(T, D, dev) if N is None else _out(N, (T, D), E4M3, "N", d, dev)
-        if n_scale is None:
-            n_scale = torch.empty(((D + 127) >> 7, T), dtype=torch.float32, device=dev)
-        a.n_scale = _scales(n_scale, (D + 127) >> 7, T, "n_scale", d)
-    else:
-        N = _out(N, (T, D), out_dtype, "N", d, dev)
-    a.n_out, a.ldn = N.data_ptr(), _matrix(N, "N", d)[2]
+        n_scale, a.n_scale = _new_scales(n_scale, (D + 127) >> 7, T, "n_scale", d, dev)
     _call("mobi_norm", d, stream, ctypes.addressof(a))
     n = (N, n_scale) if odt == 3 else N
     return n if block is None else (n, R)
@@ -286,8 +279,8 @@ def mobi_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, tem
     f32 = torch.float32
     lp = None if tp is None else torch.empty(T, dtype=f32, device=dev)
     en = torch.empty(T, dtype=f32, device=dev) if entropy else None
-    top = torch.empty((T, max(k, 0)), dtype=f32, device=dev)
-    idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    top = torch.empty(T, max(k, 0), dtype=f32, device=dev)
+    idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
     _call("mobi_logprobs", d, stream, logits.data_ptr(), dt, T, V, ld, tp, temperature, k,
           None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(), top.data_ptr(),
           idx.data_ptr())
