@@ -562,7 +562,8 @@ MOBI_API mobi_status mobi_sync_check(void* stream);
  * faulting anything: the kernel records the error, drains its own copies (and
  * MMAs) in flight, frees its tensor memory and returns. Below 64 the decode
  * kernel's waits poll without suspending and each of its warps first waits on
- * a barrier that nothing completes, so its timeout path always runs.
+ * a barrier that nothing completes, so its timeout path always runs; the 8-bit
+ * products' MMA issuers do the same.
  * Test use only.
  */
 MOBI_API mobi_status mobi_debug_set_wait_limit(int64_t limit);

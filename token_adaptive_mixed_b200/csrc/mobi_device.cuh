@@ -139,6 +139,13 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// An fp32 word of the cluster's shared memory (address from map_to_rank).
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Arrival on an mbarrier of another CTA (address from map_to_rank). It hands over
 // tensor memory, which the tcgen05 fences order: no memory writes are published,
 // so the default CTA scope does. (A release at cluster scope waits for the

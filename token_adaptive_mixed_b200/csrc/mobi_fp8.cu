@@ -16,7 +16,8 @@
 // the weight rows; the promotion's scale is one register per thread. "narrow" puts
 // weight rows on the lanes (128 rows x 16..128 tokens), so that one token costs
 // a 16-wide tile and not a 128-wide one, and splits K over a cluster whose CTAs
-// add their sums through distributed shared memory in rank order.
+// read each other's sums through distributed shared memory and add them in rank
+// order.
 //
 // All mbarrier waits are bounded; on a timeout the kernel records the error,
 // drains its copies and MMAs in flight, frees TMEM and returns.
@@ -133,24 +134,18 @@ __device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* y, int
     }
     return;
   }
+  // Ragged tiles and rows that are not 16-byte aligned: an element per lane, so
+  // that a warp still writes whole sectors (T = 333, N = 4099, bf16: RAG_FIG).
+  const int rows = T - t0 < 32 ? (int)(T - t0) : 32;
+  for (int row = 0; row < rows; ++row) {
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int row = (i * 32 + lane) / CH, ch = lane % CH;
-    const int64_t t = t0 + row, n = n0 + ch * EC;
-    if (t >= T || n >= N) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + 16 * (ch ^ (row & 7)));
-    uint8_t* p = y + (t * ld + n) * ES;
-    if (vec && n + EC <= N) {
-      *reinterpret_cast<uint4*>(p) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < EC; ++e)
-        if (n + e < N) {
-          if (ES == 4) reinterpret_cast<uint32_t*>(p)[e] = w[e];
-          if (ES == 2) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
-          if (ES == 1) p[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
-        }
+    for (int c0 = 0; c0 < COLS; c0 += 32) {
+      const int c = c0 + lane, at = row * 128 + 16 * ((c / EC) ^ (row & 7)) + c % EC * ES;
+      if (n0 + c >= N) continue;
+      uint8_t* p = y + ((t0 + row) * ld + n0 + c) * ES;
+      if (ES == 4) *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(stage + at);
+      if (ES == 2) *reinterpret_cast<uint16_t*>(p) = *reinterpret_cast<const uint16_t*>(stage + at);
+      if (ES == 1) *p = stage[at];
     }
   }
 }
@@ -277,7 +272,9 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
         const uint32_t d = tmem + par * BN;
         uint32_t s = par, ph = 0, dph = 1;
         bool have = false;
-        for (int64_t it = par; it < units; it += 2) {
+        // A test-sized limit waits for what nothing completes, so that the timeout path always runs.
+        const bool go = limit >= 64 || mbar_wait_abort(&sm.drain, 0, limit, st, 0x510, abort_flag);
+        for (int64_t it = go ? par : units; it < units; it += 2) {
           if (!mbar_wait_abort(&sm.d_empty[par], dph, limit, st, 0x512, abort_flag)) break;
           if (!have && !mbar_wait_abort(&sm.full[s], ph, limit, st, 0x511, abort_flag)) break;
           tc_fence_after();
@@ -490,8 +487,7 @@ struct Cfg {
   static constexpr int ST = GATED ? (BN == 64 ? 5 : 3) : (BN == 16 ? 6 : (BN == 32 ? 5 : (BN == 64 ? 4 : 6)));
   static_assert(HC >= 8 && HC <= 64 && TMEM * kPerSm <= 512 && (TMEM & (TMEM - 1)) == 0, "tile");
   static constexpr int MT = ST >= 4 ? 2 : 1;                 // MMA threads (see there)
-  static constexpr int kRed = (COLS + 8 * MATS) * 128;       // the cluster's sums (tokens rounded up for each owner)
-  static_assert(kRed * 4 <= ST * kStage, "the cluster's sums take the stages' place");
+  static_assert(COLS * 512 <= ST * kStage, "the sums take the stages' place");
 };
 
 template <bool GATED, int BN>
@@ -502,8 +498,7 @@ struct Smem {
       uint8_t w[C::ST][C::kWBytes];      // 1024-byte aligned (offset 0)
       uint8_t x[C::ST][C::kXBytes];
     };
-    // After the last block: [source rank][owned column][row], the cluster's sums of the owned tokens.
-    float red[C::kRed];
+    float red[C::COLS * 128];            // after the last block: this CTA's sums, [column][row]
   };
   float xs[kRing][BN];                   // fetched scales of the tile's tokens and weight blocks
   float ws[kRing][2];
@@ -534,7 +529,15 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
   const int kb0 = (int)((int64_t)nkb * rank / csize), kb1 = (int)((int64_t)nkb * (rank + 1) / csize);
   const int64_t nblk = (N + 127) / 128, wb = n0 / 128;
 
-  if (threadIdx.x == 0) {
+  // The producer sets up the barriers and has the first stages on their way while
+  // the other warps get tensor memory.
+  auto load = [&](int kb, uint32_t s) {
+    mbar_arrive_expect_tx(&sm.full[s], CF::kStage);
+    tma_load_2d(&sm.w[s][0], &tm_w, kb * f8::BK, (int)n0, &sm.full[s]);
+    if (GATED) tma_load_2d(&sm.w[s][f8::kTileBytes], &tm_u, kb * f8::BK, (int)n0, &sm.full[s]);
+    tma_load_2d(&sm.x[s][0], &tm_x, kb * f8::BK, (int)t0, &sm.full[s]);
+  };
+  if (warp == 8 && lane == 0) {
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_x);
     if (GATED) prefetch_tmap(&tm_u);
@@ -543,14 +546,16 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
     fence_barrier_init();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = 0; i < CF::ST && kb0 + i < kb1; ++i) load(kb0 + i, (uint32_t)i);
   }
   if (warp == 9) tmem_alloc(&sm.tmem_base, CF::TMEM);
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   float2 acc[CF::HC / 2];
 #pragma unroll
@@ -560,15 +565,16 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
 
   if (warp == 8) {
     if (lane == 0) {
-      // ---- TMA producer ----
-      uint32_t s = 0, ph = 1;
-      int kb = kb0;
+      // ---- TMA producer (the first ST blocks are on their way) ----
+      uint32_t s = 0, ph = 0;
+      int kb = kb0 + CF::ST < kb1 ? kb0 + CF::ST : kb1;
+      if (kb - kb0 < CF::ST) {
+        s = (uint32_t)(kb - kb0);
+        ph = 1;
+      }
       for (; kb < kb1; ++kb) {
         if (!mbar_wait_abort(&sm.empty[s], ph, limit, st, 0x531, abort_flag)) break;
-        mbar_arrive_expect_tx(&sm.full[s], CF::kStage);
-        tma_load_2d(&sm.w[s][0], &tm_w, kb * f8::BK, (int)n0, &sm.full[s]);
-        if (GATED) tma_load_2d(&sm.w[s][f8::kTileBytes], &tm_u, kb * f8::BK, (int)n0, &sm.full[s]);
-        tma_load_2d(&sm.x[s][0], &tm_x, kb * f8::BK, (int)t0, &sm.full[s]);
+        load(kb, s);
         if (++s == CF::ST) {
           s = 0;
           ph ^= 1;
@@ -593,7 +599,9 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
       const uint64_t w0 = desc_sw128(smem_addr(&sm.w[0][0])), x0 = desc_sw128(smem_addr(&sm.x[0][0]));
       const int first = warp - 9;
       uint32_t s = (uint32_t)first, ph = 0, db = s, dph = 1;
-      for (int kb = first < MT ? kb0 + first : kb1; kb < kb1; kb += MT) {
+      // As in the wide kernel: a test-sized limit always runs out here.
+      const bool go = limit >= 64 || mbar_wait_abort(&sm.drain, 0, limit, st, 0x540, abort_flag);
+      for (int kb = go && first < MT ? kb0 + first : kb1; kb < kb1; kb += MT) {
         if (!mbar_wait_abort(&sm.d_empty[db], dph, limit, st, 0x542, abort_flag)) break;
         if (!mbar_wait_abort(&sm.full[s], ph, limit, st, 0x541, abort_flag)) break;
         tc_fence_after();
@@ -702,53 +710,53 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     }
   }
 
-  // The cluster's sums: CTA r owns the tokens [r tpc, (r + 1) tpc) of the tile;
-  // every CTA writes its sums of them into r's shared memory, and r adds them in
-  // rank order (the result does not depend on who finishes first). The sums take
-  // the stages' place, so every CTA is through with its blocks first.
+  // The cluster's sums. Every CTA lays its own out in its shared memory, in the
+  // stages' place (every block of its own has been read by then: the last sums
+  // say so); CTA r then reads the tokens [r tpc, (r + 1) tpc) of all of them and
+  // adds them in rank order, so the result does not depend on who finishes first.
+  if (warp < 8) {
+    float* mine = &sm.red[(half * CF::HC) * 128 + 32 * q + lane];
+#pragma unroll
+    for (int c = 0; c < CF::HC; ++c) mine[c * 128] = (c & 1) ? acc[c >> 1].y : acc[c >> 1].x;
+  }
   __syncwarp();
   cluster_arrive();
   cluster_wait();
   const int tpc = (BN + csize - 1) / csize;
   if (warp < 8) {
-    const uint32_t red = smem_addr(&sm.red[0]) + (uint32_t)(((int)rank * CF::MATS + mat) * tpc * 128 + 32 * q + lane) * 4;
-    int owner = j0 / tpc, slot = j0 % tpc;
-#pragma unroll
-    for (int c = 0; c < CF::HC; ++c) {
-      uint32_t remote;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(red + slot * 512), "r"(owner));
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"((c & 1) ? acc[c >> 1].y : acc[c >> 1].x)
-                   : "memory");
-      if (++slot == tpc) {
-        slot = 0;
-        ++owner;
-      }
-    }
-  }
-  __syncwarp();
-  cluster_arrive();
-  cluster_wait();
-
-  if (warp < 8) {
     const int row = threadIdx.x & 127;
     const int64_t n = n0 + row;
-    const int per = CF::MATS * tpc * 128;
+    uint32_t peer[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) peer[c] = map_to_rank(&sm.red[row], c < csize ? c : 0);
     for (int tl = half; tl < tpc; tl += 2) {  // tokens of this CTA, alternating between the two groups of 128 threads
-      const int64_t t = t0 + (int64_t)rank * tpc + tl;
-      if (t >= T || (int)rank * tpc + tl >= BN) break;
-      float v = 0.0f, u = 0.0f;
-      for (int c = 0; c < csize; ++c) {
-        v += sm.red[c * per + tl * 128 + row];
-        if (GATED) u += sm.red[c * per + (tpc + tl) * 128 + row];
+      const int j = (int)rank * tpc + tl;
+      const int64_t t = t0 + j;
+      if (t >= T || j >= BN) break;
+      float a[8], b[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        a[c] = b[c] = 0.0f;
+        if (c < csize) {
+          a[c] = ld_cluster(peer[c] + (uint32_t)j * 512);
+          if (GATED) b[c] = ld_cluster(peer[c] + (uint32_t)(BN + j) * 512);
+        }
       }
+      float v = a[0], u = b[0];
+#pragma unroll
+      for (int c = 1; c < 8; ++c)
+        if (c < csize) {
+          v += a[c];
+          u += b[c];
+        }
       if (GATED) v = f8::activate(v, act) * u;
       if (GATED && out.type == MOBI_E4M3) {
-        uint32_t a = __reduce_max_sync(0xffffffffu, abs_bits(v));
+        uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(v));
         uint32_t* cm = sm.colmax[half][(tl >> 1) & 1];
-        if (lane == 0) cm[q] = a;
+        if (lane == 0) cm[q] = m;
         f8::named_barrier(1 + half, 128);
-        a = max(max(cm[0], cm[1]), max(cm[2], cm[3]));
-        const float s = block_scale(a), r = 1.0f / s;
+        m = max(max(cm[0], cm[1]), max(cm[2], cm[3]));
+        const float s = block_scale(m), r = 1.0f / s;
         if (row == 0) out.scale[wb * T + t] = s;
         if (n < N) static_cast<uint8_t*>(out.y)[t * out.ld + n] = (uint8_t)e4m3x2(v * r, 0.0f);
       } else if (n < N) {
@@ -760,6 +768,10 @@ __global__ void __launch_bounds__(f8n::kThreads, f8n::Cfg<GATED, BN>::kPerSm)
     }
   }
 
+  // No CTA leaves while another may still read its sums.
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
