@@ -13,7 +13,8 @@
 // Two kernels. "wide" puts tokens on the TMEM lanes: a persistent pair of CTAs
 // (cta_group::2) per two SMs takes tiles of 256 tokens x 256 output columns (or
 // 128 gate + 128 up columns), each CTA holding half of the tokens and half of
-// the weight rows; the promotion's scale is one register per thread. "narrow" puts
+// the weight rows; the promotion's scale is one register per thread. Few tiles
+// are made twice as many of 128 columns. "narrow" puts
 // weight rows on the lanes (128 rows x 16..128 tokens), so that one token costs
 // a 16-wide tile and not a 128-wide one, and splits K over a cluster whose CTAs
 // read each other's sums through distributed shared memory and add them in rank
@@ -86,26 +87,33 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // ---- wide: tokens on lanes ---------------------------------------------------------
 
 namespace f8w {
-constexpr int ST = 5;                       // pipeline stages (one block of K each)
-constexpr int BM = 256, BN = 256;           // tokens and weight rows (or 128 gate + 128 up) of a pair's tile
-constexpr uint32_t kStage = 2 * f8::kTileBytes;  // a CTA's half of either operand
+constexpr int BM = 256;                     // tokens of a pair's tile
 constexpr int kThreads = 12 * 32;           // 0 producer, 1 and 2 MMA, 3 scales, 4-11 epilogue
 constexpr int kGroupM = 8;                  // token tiles swept together over the weight tiles (L2 reuse)
 constexpr int kRing = 8, kAhead = 6;        // fetched scales: slots, and blocks between the fetch and the use
 constexpr uint64_t kDrainLimit = 1 << 16;   // polls while the last copies land (only an abort runs them out)
 
+// BN: weight rows of a tile, 256 (gated: 128 gate + 128 up) or 128.
+template <int BN>
 struct Smem {
+  static constexpr int ST = BN == 256 ? 5 : 7;      // pipeline stages (one block of K each)
+  static constexpr int NB = 512 / BN;               // accumulator buffers in TMEM
+  static constexpr uint32_t kB = BN / 2 * f8::BK;   // a CTA's half of the weight rows
+  static constexpr uint32_t kStage = f8::kTileBytes + kB;
   uint8_t a[ST][f8::kTileBytes];            // 1024-byte aligned (offset 0)
-  uint8_t b[ST][f8::kTileBytes];
+  uint8_t b[ST][kB];
   uint8_t out[f8::kEpiWarps][32 * 128];     // per warp: 32 rows x 128 bytes, 16-byte chunk j of row r at j ^ (r & 7)
-  float xs[kRing][128];                     // fetched scales of the CTA's tokens and of the tile's two weight blocks
+  float xs[kRing][128];                     // fetched scales of the CTA's tokens and of the tile's weight blocks
   float ws[kRing][4];
-  float scale[4][2][128];                   // their products: [slot][weight block][token]
+  float scale[2 * NB][BN / 128][128];       // their products: [slot][weight block][token]
   uint32_t rowmax[2][128];                  // e4m3 output: |h| maxima of a row's two halves
   // full and d_empty are used in the first CTA of the pair (it issues the MMAs), empty and d_full in both.
-  uint64_t full[ST], empty[ST], d_full[2], d_empty[2], drain;
+  uint64_t full[ST], empty[ST], d_full[NB], d_empty[NB], drain;
   uint32_t tmem_base;
   int32_t abort_flag;
+  // A parity wait tells a phase from the one before it only. An MMA thread tests block u + 2's stage once
+  // block u's buffer is free, which says that u - NB and all before it have gone through.
+  static_assert(ST >= NB + 2, "stages");
 };
 
 // Tile index -> (token tile, weight tile): kGroupM token tiles at a time, weight
@@ -135,7 +143,7 @@ __device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* y, int
     return;
   }
   // Ragged tiles and rows that are not 16-byte aligned: an element per lane, so
-  // that a warp still writes whole sectors (T = 333, N = 4099, bf16: RAG_FIG).
+  // that a warp still writes whole sectors (T = 333, N = 4099, bf16: eight elements per lane took 32 us, this 23.8).
   const int rows = T - t0 < 32 ? (int)(T - t0) : 32;
   for (int row = 0; row < rows; ++row) {
 #pragma unroll
@@ -189,16 +197,19 @@ __device__ __forceinline__ void write_out(const float (&v)[NC], uint8_t* stage, 
 }
 }  // namespace f8w
 
-template <bool GATED>
+template <bool GATED, int BN>
 __global__ void __launch_bounds__(f8w::kThreads, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_u, const float* xs,
                     const float* ws, const float* us, int64_t T, int64_t N, int nkb, int act,
                     f8::Out out, DeviceStatus* st, uint64_t limit) {
   using namespace f8w;
-  constexpr int TN = GATED ? 128 : 256;  // output columns of a tile
+  static_assert(BN == 256 || (BN == 128 && !GATED), "tile");
+  using SM = Smem<BN>;
+  constexpr int TN = GATED ? 128 : BN;  // output columns of a tile
+  constexpr int ST = SM::ST, NB = SM::NB, WB = BN / 128;  // WB: weight blocks of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int32_t* abort_flag = &sm.abort_flag;
   const uint32_t rank = cluster_rank();
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) { mbar_init(&sm.full[i], 1); mbar_init(&sm.empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&sm.d_full[i], 2); mbar_init(&sm.d_empty[i], 2 * f8::kEpiWarps); }
+    for (int i = 0; i < NB; ++i) { mbar_init(&sm.d_full[i], 2); mbar_init(&sm.d_empty[i], 2 * f8::kEpiWarps); }
     mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -238,10 +249,10 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       for (int64_t i = first; i < ntiles && ok; i += stride) {
         int64_t m, n;
         tile_at(i, n_mt, n_nt, &m, &n);
-        const int xr = (int)(m * BM) + 128 * rank, wr = (int)(n * TN) + (GATED ? 0 : 128 * rank);
+        const int xr = (int)(m * BM) + 128 * rank, wr = (int)(n * TN) + (GATED ? 0 : BN / 2 * rank);
         for (int kb = 0; kb < nkb; ++kb, ++issued) {
           if (!(ok = mbar_wait_abort(&sm.empty[s], ph, limit, st, 0x501, abort_flag))) break;
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * SM::kStage);
           const uint32_t bar = full0 + s * 8;
           tma_load_2d_pair(&sm.a[s][0], &tm_x, kb * f8::BK, xr, bar);
           tma_load_2d_pair(&sm.b[s][0], tw, kb * f8::BK, wr, bar);
@@ -258,29 +269,29 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
         mbar_wait(&sm.empty[s], ph ^ 1, kDrainLimit, st, 0x5F1);
       }
     } else if (warp == 1 || warp == 2) {
-      // ---- MMA issuers, for both CTAs: warp 1 takes the even blocks (D buffer 0), warp 2 the odd ones ----
+      // ---- MMA issuers, for both CTAs: warp 1 takes the even blocks, warp 2 the odd ones ----
       // Issuing waits for room in the tensor pipe's short queue, a barrier check
       // takes about 100 clocks even where it is ready, and a commit half of that:
       // one thread alone left the pipe idle for half of the time. Each thread
-      // tests the next block's stage while it issues this one: that asks for block
-      // u + 2's phase of its stage, which block u - 3 used before; block u's buffer
-      // being free says that u - 2 and all before it have gone through.
+      // tests its next block's stage while it issues this one.
       if (lane == 0 && rank == 0) {
         constexpr uint32_t idesc = idesc_e4m3(BM, BN);
         const uint64_t a0 = desc_sw128(smem_addr(&sm.a[0][0])), b0 = desc_sw128(smem_addr(&sm.b[0][0]));
-        const int par = warp - 1;
-        const uint32_t d = tmem + par * BN;
-        uint32_t s = par, ph = 0, dph = 1;
+        uint32_t s = (uint32_t)(warp - 1), ph = 0, db = s, dph = 1;
         bool have = false;
         // A test-sized limit waits for what nothing completes, so that the timeout path always runs.
         const bool go = limit >= 64 || mbar_wait_abort(&sm.drain, 0, limit, st, 0x510, abort_flag);
-        for (int64_t it = go ? par : units; it < units; it += 2) {
-          if (!mbar_wait_abort(&sm.d_empty[par], dph, limit, st, 0x512, abort_flag)) break;
+        for (int64_t it = go ? warp - 1 : units; it < units; it += 2) {
+          if (!mbar_wait_abort(&sm.d_empty[db], dph, limit, st, 0x512, abort_flag)) break;
           if (!have && !mbar_wait_abort(&sm.full[s], ph, limit, st, 0x511, abort_flag)) break;
           tc_fence_after();
-          const uint32_t s0 = s;
-          const uint64_t a = a0 + s * (f8::kTileBytes / 16), b = b0 + s * (f8::kTileBytes / 16);
-          dph ^= 1;
+          const uint32_t s0 = s, db0 = db, d = tmem + db * BN;
+          const uint64_t a = a0 + s * (f8::kTileBytes / 16), b = b0 + s * (SM::kB / 16);
+          db += 2;
+          if (db >= NB) {
+            db -= NB;
+            dph ^= 1;
+          }
           s += 2;
           if (s >= ST) {
             s -= ST;
@@ -291,7 +302,7 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
           mma_ss_f8_pair<true>(d, a + 2, b + 2, idesc);
           mma_ss_f8_pair<true>(d, a + 4, b + 4, idesc);
           mma_ss_f8_pair<true>(d, a + 6, b + 6, idesc);
-          mma_commit_pair(&sm.d_full[par]);
+          mma_commit_pair(&sm.d_full[db0]);
           mma_commit_pair(&sm.empty[s0]);
         }
         mma_commit_pair_local(&sm.drain);  // every MMA issued is done before TMEM is released
@@ -312,9 +323,9 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
         px = xs + t;
 #pragma unroll
         for (int j = 0; j < 4; ++j) in[j] = t + 32 * j < T;
-        // Plain: the tile's columns are weight blocks 2 n and 2 n + 1 (where the
-        // tile ends before the second, its sums are not written). Gated: block n of either matrix.
-        const int64_t wb = GATED ? n : (2 * n + lane < nblk ? 2 * n + lane : nblk - 1);
+        // Plain: the tile's columns are weight blocks WB n .. (where the tile ends
+        // before the second, its sums are not written). Gated: block n of either matrix.
+        const int64_t wb = GATED ? n : (WB * n + lane < nblk ? WB * n + lane : nblk - 1);
         pw = (GATED && lane == 1 ? us : ws) + wb;
       };
       auto fetch = [&](int64_t unit) {
@@ -324,7 +335,7 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (in[j]) copy4_async(&sm.xs[slot][lane + 32 * j], px + 32 * j);
-          if (lane < 2) copy4_async(&sm.ws[slot][lane], pw);
+          if (lane < WB) copy4_async(&sm.ws[slot][lane], pw);
           px += T;
           pw += nblk;
           if (++fkb == nkb) {
@@ -336,21 +347,21 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       };
       for (int j = 0; j < kAhead; ++j) fetch(j);
       for (int64_t it = 0; it < units; ++it) {
-        // The slot's last reader was block it - 4; block it - 2 having its sums says that it is done.
-        if (it >= 2 && !mbar_wait_abort_warp(&sm.d_full[it & 1], ((it - 2) >> 1) & 1, limit, st, 0x561, abort_flag))
+        // The slot's last readers took block it - 2 NB; block it - NB having its sums says that they are done.
+        if (it >= NB && !mbar_wait_abort_warp(&sm.d_full[it % NB], (it / NB - 1) & 1, limit, st, 0x561, abort_flag))
           break;
         copy_async_wait<kAhead - 1>();
         __syncwarp();
         const int slot = (int)(it % kRing);
-        const float w0 = sm.ws[slot][0], w1 = sm.ws[slot][1];
+        float(*to)[128] = sm.scale[it % (2 * NB)];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x = sm.xs[slot][lane + 32 * j];
-          sm.scale[it & 3][0][lane + 32 * j] = x * w0;
-          sm.scale[it & 3][1][lane + 32 * j] = x * w1;
+        for (int w = 0; w < WB; ++w) {
+          const float f = sm.ws[slot][w];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) to[w][lane + 32 * j] = sm.xs[slot][lane + 32 * j] * f;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.d_full[it & 1]);
+        if (lane == 0) mbar_arrive(&sm.d_full[it % NB]);
         fetch(it + kAhead);
       }
       copy_async_wait<0>();
@@ -370,20 +381,23 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       int64_t m, n;
       tile_at(i, n_mt, n_nt, &m, &n);
       const int64_t trow = m * BM + 128 * rank + 32 * q, t = trow + lane;
-      float2 acc[2][32];  // plain: 64 + 64 columns; gated: 64 gate columns, the same 64 up columns
+      float2 acc[WB][32];  // plain: 64 (+ 64) columns; gated: 64 gate columns, the same 64 up columns
 #pragma unroll
-      for (int c = 0; c < 32; ++c) acc[0][c] = acc[1][c] = make_float2(0.0f, 0.0f);
+      for (int w = 0; w < WB; ++w)
+#pragma unroll
+        for (int c = 0; c < 32; ++c) acc[w][c] = make_float2(0.0f, 0.0f);
       for (int kb = 0; kb < nkb && ok; ++kb) {
-        const uint32_t db = it & 1;
-        if (!(ok = mbar_wait_abort_warp(&sm.d_full[db], (it >> 1) & 1, limit, st, 0x521, abort_flag))) break;
+        const uint32_t db = it % NB;
+        if (!(ok = mbar_wait_abort_warp(&sm.d_full[db], (it / NB) & 1, limit, st, 0x521, abort_flag))) break;
         tc_fence_after();
-        const float sc[2] = {sm.scale[it & 3][GATED ? 0 : half][32 * q + lane],
-                             GATED ? sm.scale[it & 3][1][32 * q + lane] : 0.0f};
+        const float(*from)[128] = sm.scale[it % (2 * NB)];
+        const float s0 = from[GATED || WB == 1 ? 0 : half][32 * q + lane];
+        const float s1 = GATED ? from[WB - 1][32 * q + lane] : s0;
         ++it;
         // Loads of CW columns, each in flight while the one before is added; the
         // buffer is released as soon as the last has arrived.
-        constexpr int CW = 16, NC = 128 / CW;
-        const uint32_t d = tmem + lane_addr + db * BN + half * (GATED ? 64 : 128);
+        constexpr int CW = 16, NC = BN / 2 / CW;
+        const uint32_t d = tmem + lane_addr + db * BN + half * (GATED ? 64 : BN / 2);
         uint32_t r[2][CW];
         tmem_ld16(d, r[0]);
 #pragma unroll
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
             if (lane == 0) mbar_arrive_remote(d_empty0 + db * 8);
           }
           const int h = c * CW / 64;
-          const float v = GATED ? sc[h] : sc[0];
+          const float v = h ? s1 : s0;
           const float2 s2 = make_float2(v, v);
 #pragma unroll
           for (int j = 0; j < CW / 2; ++j) {
@@ -409,9 +423,10 @@ __global__ void __launch_bounds__(f8w::kThreads, 1)
       }
       if constexpr (!GATED) {
         if (ok) {
-          const int64_t n0 = n * 256 + 128 * half;
+          const int64_t n0 = n * BN + BN / 2 * half;
           write_out<64>(reinterpret_cast<const float(&)[64]>(acc[0]), stage, out, trow, T, n0, N, lane);
-          write_out<64>(reinterpret_cast<const float(&)[64]>(acc[1]), stage, out, trow, T, n0 + 64, N, lane);
+          if (WB == 2)
+            write_out<64>(reinterpret_cast<const float(&)[64]>(acc[WB - 1]), stage, out, trow, T, n0 + 64, N, lane);
         }
       } else {
         float h[64];
@@ -791,34 +806,60 @@ struct Fp8Job {
   int act;
 };
 
-// Which kernel and, for the narrow one, the token tile and the cluster.
+// Which kernel, its token tile (narrow) or weight tile (wide), and the narrow one's cluster.
 struct Fp8Plan {
   bool wide;
   int bn, csize;
 };
 
-// Narrow: the token tile is the batch rounded up, to 128 (gated 64) at most,
-// and K is cut over as many CTAs as fit at once, two blocks each at least.
-// From 33 tokens on both kernels' times are estimated from their waves and
-// blocks: measured at K = 4096 (N = 4096 and 11008, T = 64 .. 1024), the wide
-// kernel takes 0.52 us a block and wave (fewer SMs, but a quarter of the time per
-// output) and the narrow one 0.85 us a block of its CTA's share. T = 333,
-// N = 4099: 20 us against 32; T = 64, N = 11008: 22 us against 16.
+// Clusters of c = 1 .. 8 CTAs that run at once, one CTA to an SM (what
+// cudaOccupancyMaxActiveClusters answers on a B200's 148 SMs).
+constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+
+// The narrow kernel's token tile is the batch rounded up, to 128 (gated 64) at
+// most. K is cut over a cluster, two blocks of 128 to a CTA at least: up to the
+// device's room where two CTAs share an SM (T = 1, N = K = 4096, clusters of 8, 4,
+// 2: 6.2, 6.9, 8.6 us; T = 8, gated, N = 11008: clusters of 3, 2, 4: 18.6, 22.3,
+// 23.6 us), by the fewest blocks in a row where one does.
+// From 33 tokens on the kernels' times are estimated from their waves and
+// blocks, in units of 10 ns fitted at K = 4096 and 11008, N = 1024, 4096 and 11008,
+// T = 64 .. 2048. Measured at K = 4096, in us, narrow / wide with 128 and with
+// 256 weight rows: T = 64, N = 11008: 15.2 / 23.2 / 22; T = 333, N = 4096: 32 /
+// 14.0 / 20.6; T = 256, N = 11008: - / 24.1 / 22.8; T = 2048, N = 4096: - / 47 / 38.6.
 static Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   Fp8Plan p;
-  const int64_t nkb = (K + 127) / 128, nt = (N + 127) / 128;
-  p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || gated ? 64 : 128));
-  const int64_t tiles = nt * ((T + p.bn - 1) / p.bn);
-  const int64_t room = (p.bn * (gated ? 2 : 1) <= 64 ? 2 : 1) * (int64_t)sms;
-  int64_t c = room / tiles;
-  if (c > nkb / 2) c = nkb / 2;
-  p.csize = (int)(c < 1 ? 1 : (c > 8 ? 8 : c));
+  const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  const int64_t nkb = up(K, 128), nt = up(N, 128), mt = up(T, f8w::BM);
   p.wide = false;
-  if (T > 32) {
-    const int64_t wt = ((T + f8w::BM - 1) / f8w::BM) * (gated ? nt : (nt + 1) / 2);
-    const int64_t wide = 450 + (wt + sms / 2 - 1) / (sms / 2) * nkb * 52;
-    const int64_t narrow = 600 + (tiles * p.csize + room - 1) / room * ((nkb + p.csize - 1) / p.csize) * 85;
-    p.wide = wide < narrow;
+  p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || gated ? 64 : 128));
+  const int64_t tiles = nt * up(T, p.bn);
+  int64_t row, waves = 1;  // blocks in a row of a CTA, CTAs in a row on an SM
+  if (p.bn * (gated ? 2 : 1) <= 64) {
+    int64_t c = 2 * (int64_t)sms / tiles;
+    if (c > nkb / 2) c = nkb / 2;
+    p.csize = (int)(c < 1 ? 1 : (c > 8 ? 8 : c));
+    row = up(nkb, p.csize);
+    waves = up(tiles * p.csize, 2 * (int64_t)sms);
+  } else {
+    p.csize = 1;
+    row = nkb;
+    waves = up(tiles, kClusters[1]);
+    for (int c = 2; c <= 8 && 2 * c <= nkb; ++c) {
+      const int64_t r = up(nkb, c), w = up(tiles, kClusters[c]);
+      if (w * r < waves * row) {
+        p.csize = c;
+        row = r;
+        waves = w;
+      }
+    }
+  }
+  if (T <= 32) return p;
+  const int64_t narrow = 600 + waves * row * 85;
+  const int64_t wide256 = 450 + nkb * (56 * up(mt * (gated ? nt : up(nt, 2)), sms / 2) - 6);
+  const int64_t wide128 = gated ? wide256 : 400 + nkb * (34 * up(mt * nt, sms / 2) - 4);
+  if (wide256 < narrow || wide128 < narrow) {
+    p.wide = true;
+    p.bn = wide128 < wide256 ? 128 : 256;
   }
   return p;
 }
@@ -837,6 +878,20 @@ static cudaError_t launch_narrow(const Fp8Job& j, const Fp8Plan& p, const CUtens
   return note_error("fp8 narrow launch", e);
 }
 
+template <bool GATED, int BN>
+static cudaError_t launch_wide(const Fp8Job& j, const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mu,
+                               cudaStream_t stream, DeviceStatus* st) {
+  constexpr int smem = (int)sizeof(f8w::Smem<BN>) + 1024, TN = GATED ? 128 : BN;
+  static_assert(smem <= 232448, "shared memory");
+  cudaError_t e = set_smem((const void*)fp8_wide_kernel<GATED, BN>, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((j.T + f8w::BM - 1) / f8w::BM) * ((j.N + TN - 1) / TN), pairs = num_sms() / 2;
+  e = launch_dependent(fp8_wide_kernel<GATED, BN>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), f8w::kThreads,
+                       smem, 2, stream, mx, mw, mu, j.xs, j.ws, j.us, j.T, j.N, (int)((j.K + 127) / 128), j.act, j.out,
+                       st, wait_limit());
+  return note_error("fp8 wide launch", e);
+}
+
 template <bool GATED>
 static cudaError_t launch_fp8(const Fp8Job& j, cudaStream_t stream) {
   cudaError_t e;
@@ -845,7 +900,7 @@ static cudaError_t launch_fp8(const Fp8Job& j, cudaStream_t stream) {
   const int sms = num_sms();
   const Fp8Plan p = fp8_plan(j.T, j.N, j.K, GATED, sms);
   CUtensorMap mx, mw, mu = {};
-  const uint32_t rows_x = p.wide ? 128 : (uint32_t)p.bn, rows_w = 128;
+  const uint32_t rows_x = p.wide ? 128 : (uint32_t)p.bn, rows_w = p.wide && p.bn == 128 ? 64 : 128;
   if (!make_tmap_u8(&mx, j.X, (uint64_t)j.K, (uint64_t)j.T, (uint64_t)j.ldx, rows_x) ||
       !make_tmap_u8(&mw, j.W, (uint64_t)j.K, (uint64_t)j.N, (uint64_t)j.ldw, rows_w) ||
       (GATED && !make_tmap_u8(&mu, j.U, (uint64_t)j.K, (uint64_t)j.N, (uint64_t)j.ldu, rows_w)))
@@ -860,16 +915,9 @@ static cudaError_t launch_fp8(const Fp8Job& j, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     }
   }
-  constexpr int smem = (int)sizeof(f8w::Smem) + 1024;
-  static_assert(smem <= 232448, "shared memory");
-  e = set_smem((const void*)fp8_wide_kernel<GATED>, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = ((j.T + f8w::BM - 1) / f8w::BM) * ((j.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  e = launch_dependent(fp8_wide_kernel<GATED>, dim3((unsigned)(2 * pairs)), f8w::kThreads, smem, 2,
-                       stream, mx, mw, mu, j.xs, j.ws, j.us, j.T, j.N, (int)((j.K + 127) / 128), j.act, j.out, st,
-                       wait_limit());
-  return note_error("fp8 wide launch", e);
+  if constexpr (!GATED)
+    if (p.bn == 128) return launch_wide<false, 128>(j, mx, mw, mu, stream, st);
+  return launch_wide<GATED, 256>(j, mx, mw, mu, stream, st);
 }
 
 namespace {
