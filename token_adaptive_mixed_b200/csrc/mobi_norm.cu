@@ -351,20 +351,22 @@ struct RawOct {
   }
 };
 
-__device__ __forceinline__ Oct load_oct(const void* base, int dtype, int64_t at) {
+// Weights, biases and gates have a type known at run time only. bf16 is inline;
+// the others are calls, since inlined their conversions were run beside bf16's.
+__device__ __noinline__ Oct load_oct_other(const void* base, int dtype, int64_t at) {
   if (dtype == MOBI_F32) {
     RawOct<MOBI_F32> r;
     r.load(static_cast<const float*>(base) + at);
     return r.widen();
   }
-  const uint16_t* q = static_cast<const uint16_t*>(base) + at;
-  if (dtype == MOBI_BF16) {
-    RawOct<MOBI_BF16> r;
-    r.load(q);
-    return r.widen();
-  }
   RawOct<MOBI_F16> r;
-  r.load(q);
+  r.load(static_cast<const __half*>(base) + at);
+  return r.widen();
+}
+__device__ __forceinline__ Oct load_oct(const void* base, int dtype, int64_t at) {
+  if (dtype != MOBI_BF16) return load_oct_other(base, dtype, at);
+  RawOct<MOBI_BF16> r;
+  r.load(static_cast<const __nv_bfloat16*>(base) + at);
   return r.widen();
 }
 
