@@ -16,8 +16,10 @@
 // Top alternatives without a second pass over the row: neighbouring threads
 // form 128 groups, and the k-th largest of the groups' maxima (k <= 32) is a bound tau
 // that at least k entries reach. Only groups whose maximum reaches it can hold
-// one, so about k/128 of the row is read again (from L2), the entries >= tau are
-// gathered and ranked. Many equal entries would overflow the gather: then the
+// one, so about k/128 of the row is read again, and the entries >= tau are
+// gathered and ranked. (Keeping entries as they come by, against a bound from the first
+// loads, made fp32 rows that L2 cannot hold faster, 272 to 195 us at T = 2048, V = 128000,
+// and bf16 rows slower, 108 to 146 us at V = 128001.) Many equal entries would overflow the gather: then the
 // entries above tau are gathered and the first ones equal to it are found in
 // index order. Where that does not do (even those overflow, or fewer than k
 // groups have an entry above the floor, as under a mask of the type's lowest
@@ -38,7 +40,7 @@ namespace lp {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Group g is the threads 32 (g / 16) + g % 16 and the same + 16: lanes l and l + 16 of a warp.
+// Group g is lanes 2 (g % 16) and the next of warp g / 16: 32 bytes in a row of every load, one sector when read again.
 constexpr int kGroups = kThreads / 2;
 constexpr int kMaxK = 32;
 constexpr int kCap = 1024;   // gathered candidates
@@ -264,14 +266,14 @@ __device__ void gather(Smem& sm, const Part<E>& p, float tau, bool strict) {
   __syncthreads();
   const int ng = sm.groups, per = (p.chunks + kThreads - 1) / kThreads;  // chunks of a thread
   for (int g = warp; g < ng; g += kWarps) {
-    const int id = sm.list[g], base = 32 * (id / 16) + id % 16;
+    const int id = sm.list[g], base = 32 * (id / 16) + 2 * (id % 16);
     for (int j0 = lane; j0 < 2 * per; j0 += 4 * 32) {
       uint4 r[4];
       int at[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int j = j0 + 32 * u;
-        at[u] = (j >> 1) * kThreads + base + 16 * (j & 1);
+        at[u] = (j >> 1) * kThreads + base + (j & 1);
         if (at[u] < p.chunks) r[u] = p.raw(at[u]);
       }
 #pragma unroll
@@ -485,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 6)
   }
 
   if (k > 0) {
-    const float g = fmaxf(a.m, __shfl_xor_sync(0xffffffffu, a.m, 16));
+    const float pair = fmaxf(a.m, __shfl_xor_sync(0xffffffffu, a.m, 1));
+    const float g = __shfl_sync(0xffffffffu, pair, 2 * tid & 31);  // lanes 0 .. 15 hold the warp's groups in order
     if ((tid & 31) < 16) sm.gmax[16 * (tid >> 5) + (tid & 31)] = g;
   }
   block_join(sm, a, c);
