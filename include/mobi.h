@@ -665,7 +665,8 @@ typedef struct mobi_norm_args {
  * x, block, gate and the weights are MOBI_F32, MOBI_BF16 or MOBI_F16; n also
  * MOBI_E4M3. Every pointer is aligned to its element (16-byte aligned rows are read and
  * written faster). T = 0: nothing. D from 1 to 16384 (MOBI_ERR_UNSUPPORTED_SHAPE beyond),
- * T <= 2^28; pitches >= D; eps, post_eps >= 0 and scale finite. Outputs do not overlap the inputs or each
+ * T <= 2^28; pitches >= D; eps, post_eps >= 0 and scale finite. Squares are summed in fp32: rows with values
+ * beyond about 1e18 overflow to a norm of 0, and a zero row needs eps > 0. Outputs do not overlap the inputs or each
  * other, except r_out = x with the same pitch.
  */
 MOBI_API mobi_status mobi_norm(const mobi_norm_args* args, void* stream);

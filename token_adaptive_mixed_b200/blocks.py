@@ -5,7 +5,9 @@ scoring of logits. Bindings of the calls of the same names in include/mobi.h.
 Unlike the mixed-bit calls these take row pitches, so a tensor may be a slice of
 a larger one as long as its last dimension is contiguous, and they run on the
 tensors' device, on that device's current stream (or `stream`). Tensors of one
-call live on one device. Outputs are allocated unless given.
+call live on one device. Outputs are allocated (on the current stream) unless
+given; with `stream` the caller keeps the tensors alive until that stream is
+through with them, as for any work queued on another stream.
 """
 from __future__ import annotations
 
