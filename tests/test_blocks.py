@@ -101,7 +101,8 @@ def test_binding_takes_cuda_tensors_only():
     q, s = x.to(torch.float8_e4m3fn), torch.ones(1, 4)
     for f in (lambda: mobi.mobi_fp8_quant(x), lambda: mobi.mobi_fp8_gemm(q, s, q, s),
               lambda: mobi.mobi_fp8_gated(q, s, q, s, q, s), lambda: mobi.mobi_norm(x),
-              lambda: mobi.mobi_logprobs(x)):
+              lambda: mobi.mobi_logprobs(x), lambda: mobi.mobi_fp8_quant(x, stream=0),
+              lambda: mobi.mobi_norm(x, stream=0)):
         with pytest.raises(ValueError):
             f()
 

@@ -536,3 +536,60 @@ def test_captured_and_replayed(mobi, T):
         for b, out in zip(bufs, got):
             for a, e in zip(out, run(*b)):
                 assert torch.equal(a.contiguous().view(torch.uint8), e.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_given_stream(mobi, handle):
+    """Calls on a given stream, or on its handle, give what they give on the current one, and their new outputs stay out
+    of memory that the current stream has freed (work queued there may still use it)."""
+    g = gen(21)
+    x, xs = ref.operand(70, 512, 1, g, device=DEV)
+    w, ws = ref.operand(384, 512, 128, g, device=DEV)
+    v = torch.randn(70, 512, generator=g).to(DEV)
+    y = torch.randint(0, 512, (70,), generator=g).to(DEV)
+    calls = [lambda **k: mobi.mobi_fp8_quant(v, **k), lambda **k: (mobi.mobi_fp8_gemm(x, xs, w, ws, **k),),
+             lambda **k: (mobi.mobi_fp8_gated(x, xs, w, ws, w, ws, **k),), lambda **k: mobi.mobi_norm(v, block=v, **k),
+             lambda **k: mobi.mobi_logprobs(v, y, top_k=4, **k)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = call()
+        freed = [torch.empty_like(o) for o in want]
+        at = {o.data_ptr() for o in freed}
+        torch.cuda.synchronize()
+        del freed
+        got = call(stream=side.cuda_stream if handle else side)
+        torch.cuda.synchronize()
+        assert not at & {o.data_ptr() for o in got}
+        for a, b in zip(got, want):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    out = torch.empty(70, 384, device=DEV)
+    torch.cuda.synchronize()
+    assert mobi.mobi_fp8_gemm(x, xs, w, ws, Y=out, stream=0) is out
+    torch.cuda.synchronize()
+    assert torch.equal(out, mobi.mobi_fp8_gemm(x, xs, w, ws))
+    mobi.mobi_sync_check()
+
+
+def test_graphs_replayed_at_once(mobi):
+    """Two captured chains replayed on two streams at the same time: nothing is shared between them."""
+    run, _, _, rnd, V = _layer(mobi, 40, 13)
+    args = [(rnd(40, 256).bfloat16(), rnd(40, 256), torch.randint(0, V, (40,), generator=gen(i)).to(DEV))
+            for i in range(2)]
+    want = [run(*a) for a in args]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a in args:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(run(*a))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    mobi.mobi_sync_check()
+    for out, w in zip(outs, want):
+        for a, b in zip(out, w):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))

@@ -4,10 +4,12 @@ scoring of logits. Bindings of the calls of the same names in include/mobi.h.
 
 Unlike the mixed-bit calls these take row pitches, so a tensor may be a slice of
 a larger one as long as its last dimension is contiguous, and they run on the
-tensors' device, on that device's current stream (or `stream`). Tensors of one
-call live on one device. Outputs are allocated (on the current stream) unless
-given; with `stream` the caller keeps the tensors alive until that stream is
-through with them, as for any work queued on another stream.
+tensors' device, on that device's current stream. Tensors of one call live on
+one device. Outputs are allocated unless given. With `stream` (a stream of that
+device, or its handle) the whole call runs as under torch.cuda.stream(stream):
+new outputs belong to that stream too, since memory that the current stream has
+freed may still be in use by work queued there. The inputs are kept alive, and
+ready, by the caller, as for any work queued on another stream.
 """
 from __future__ import annotations
 
@@ -52,20 +54,27 @@ SYMBOLS = ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_norm", "mo
 _calls: dict = {}
 
 
-def _call(name: str, device: int, stream, *args) -> None:
-    """Run library call `name` on `device`, its last argument the stream."""
+def _under(stream, t: torch.Tensor):
+    """What makes `stream` the current one for a call on t's device."""
+    _on(t, "the input")
+    if not hasattr(stream, "cuda_stream"):
+        h = int(stream)
+        stream = torch.cuda.ExternalStream(h, device=t.device) if h else torch.cuda.default_stream(t.device)
+    elif stream.device != t.device:
+        raise ValueError("the stream is of another device")
+    return torch.cuda.stream(stream)
+
+
+def _call(name: str, device: int, *args) -> None:
+    """Run library call `name` on `device`, its last argument that device's current stream."""
     fn = _calls.get(name)
     if fn is None:
         from . import lib
         fn = _calls[name] = getattr(lib(), name)
     if _get_device() != device:
         with torch.cuda.device(device):
-            return _call(name, device, stream, *args)
-    if stream is None:
-        s = _raw_stream(device)
-    else:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    status = fn(*args, s)
+            return _call(name, device, *args)
+    status = fn(*args, _raw_stream(device))
     if status:
         from . import _check
         _check(name, status)
@@ -137,6 +146,9 @@ def mobi_fp8_quant(X: torch.Tensor, block_rows: int = 1, Q: torch.Tensor | None 
                    scale: torch.Tensor | None = None, stream=None):
     """X [T, K] (fp32, bf16 or fp16) in blocks of 1 x 128 (activations) or 128 x 128 (block_rows=128, weights)
     -> (Q e4m3 [T, K], scale fp32 [ceil(K/128), ceil(T/block_rows)]); Q * scale stands for X."""
+    if stream is not None:
+        with _under(stream, X):
+            return mobi_fp8_quant(X, block_rows, Q, scale)
     T, K, ldx = _matrix(X, "X")
     dt = _DT.get(X.dtype, 3)
     if dt == 3:
@@ -147,7 +159,7 @@ def mobi_fp8_quant(X: torch.Tensor, block_rows: int = 1, Q: torch.Tensor | None 
     kb, rb = (K + 127) >> 7, T if block_rows == 1 else (T + 127) >> 7
     Q, ldq = _out(Q, T, K, E4M3, "Q", d, dev)
     scale, sp = _new_scales(scale, kb, rb, "scale", d, dev)
-    _call("mobi_fp8_quant", d, stream, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), ldq, sp)
+    _call("mobi_fp8_quant", d, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), ldq, sp)
     return Q, scale
 
 
@@ -167,6 +179,9 @@ def mobi_fp8_gemm(X: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, ws: torch.
                   Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The 8-bit layer Y = X W^T: X e4m3 [T, K] with xs (block_rows=1), W e4m3 [N, K] with ws (block_rows=128)
     -> Y [T, N] in out_dtype (fp32, bf16 or fp16)."""
+    if stream is not None:
+        with _under(stream, X):
+            return mobi_fp8_gemm(X, xs, W, ws, out_dtype, Y)
     d = X.get_device()
     K = X.shape[-1]
     T, ldx, xp, xsp = _operand(X, xs, "X", 1, None, None)
@@ -175,7 +190,7 @@ def mobi_fp8_gemm(X: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, ws: torch.
     if dt == 3:
         raise ValueError("out_dtype must be fp32, bf16 or fp16")
     Y, ldy = _out(Y, T, N, out_dtype, "Y", d, X.device)
-    _call("mobi_fp8_gemm", d, stream, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), ldy)
+    _call("mobi_fp8_gemm", d, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), ldy)
     return Y
 
 
@@ -184,6 +199,9 @@ def mobi_fp8_gated(X: torch.Tensor, xs: torch.Tensor, Wg: torch.Tensor, gs: torc
                    hs: torch.Tensor | None = None, stream=None):
     """act(X Wg^T) * (X Wu^T) in one kernel, operands as mobi_fp8_gemm; act "silu", "gelu", "gelu_tanh" or "relu".
     -> H [T, N] in out_dtype, or (H e4m3, hs fp32 [ceil(N/128), T]) for out_dtype torch.float8_e4m3fn."""
+    if stream is not None:
+        with _under(stream, X):
+            return mobi_fp8_gated(X, xs, Wg, gs, Wu, us, act, out_dtype, H, hs)
     d, dev = X.get_device(), X.device
     K = X.shape[-1]
     T, ldx, xp, xsp = _operand(X, xs, "X", 1, None, None)
@@ -200,7 +218,7 @@ def mobi_fp8_gated(X: torch.Tensor, xs: torch.Tensor, Wg: torch.Tensor, gs: torc
     hsp = None
     if dt == 3:
         hs, hsp = _new_scales(hs, (N + 127) >> 7, T, "hs", d, dev)
-    _call("mobi_fp8_gated", d, stream, xp, ldx, xsp, T, K, gp, ldg, gsp, up, ldu, usp, N, _ACT[act], dt, H.data_ptr(),
+    _call("mobi_fp8_gated", d, xp, ldx, xsp, T, K, gp, ldg, gsp, up, ldu, usp, N, _ACT[act], dt, H.data_ptr(),
           ldh, hsp)
     return (H, hs) if dt == 3 else H
 
@@ -216,6 +234,10 @@ def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     x [T, D] is the residual stream, block [T, D] the block's output (None: a plain norm of x), gate anything that
     broadcasts to [T, D]; kind and post are "rms", "layer" or "none". -> (n, r), or n alone without a block; n is
     a pair (codes, scales) for out_dtype torch.float8_e4m3fn. R=x updates the residual stream in place."""
+    if stream is not None:
+        with _under(stream, x):
+            return mobi_norm(x, weight, bias, eps, kind, block, post, post_weight, post_bias, post_eps, gate, scale,
+                             unit_offset, out_dtype, N, n_scale, R)
     T, D, ldx = _matrix(x, "x")
     d, dev = x.get_device(), x.device
     xdt, odt = _DT.get(x.dtype, 3), _DT.get(out_dtype)
@@ -261,7 +283,7 @@ def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     a.n_out = N.data_ptr()
     if odt == 3:
         n_scale, a.n_scale = _new_scales(n_scale, (D + 127) >> 7, T, "n_scale", d, dev)
-    _call("mobi_norm", d, stream, ctypes.addressof(a))
+    _call("mobi_norm", d, ctypes.addressof(a))
     n = (N, n_scale) if odt == 3 else N
     return n if block is None else (n, R)
 
@@ -271,6 +293,9 @@ def mobi_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, tem
     """Scoring of logits [T, V] (fp32, bf16 or fp16) -> (logprob [T] of the int64 targets, entropy [T],
     top_logprob [T, top_k], top_index int32 [T, top_k]); logprob is None without targets, entropy without
     entropy=True. A negative target is ignored (log probability 0); one >= V is reported by mobi_sync_check."""
+    if stream is not None:
+        with _under(stream, logits):
+            return mobi_logprobs(logits, targets, temperature, top_k, entropy)
     T, V, ld = _matrix(logits, "logits")
     d, dev = logits.get_device(), logits.device
     dt = _DT.get(logits.dtype, 3)
@@ -283,7 +308,7 @@ def mobi_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, tem
     en = torch.empty(T, dtype=f32, device=dev) if entropy else None
     top = torch.empty(T, max(k, 0), dtype=f32, device=dev)
     idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
-    _call("mobi_logprobs", d, stream, logits.data_ptr(), dt, T, V, ld, tp, temperature, k,
+    _call("mobi_logprobs", d, logits.data_ptr(), dt, T, V, ld, tp, temperature, k,
           None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(), top.data_ptr(),
           idx.data_ptr())
     return lp, en, top, idx

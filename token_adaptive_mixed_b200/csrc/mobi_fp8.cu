@@ -501,6 +501,9 @@ struct Cfg {
   // Stages: about 100 KB (two CTAs) or 190 KB in flight, which covers the memory's latency at its bandwidth.
   static constexpr int ST = GATED ? (BN == 64 ? 5 : 3) : (BN == 16 ? 6 : (BN == 32 ? 5 : (BN == 64 ? 4 : 6)));
   static_assert(HC >= 8 && HC <= 64 && TMEM * kPerSm <= 512 && (TMEM & (TMEM - 1)) == 0, "tile");
+  // CTAs of any of these kernels that fit an SM together (228 KB) fit its 512 columns together. Otherwise two clusters
+  // of concurrent calls could each hold columns that the other's CTAs wait for, and the allocation waits without limit.
+  static_assert(kPerSm == 2 ? ST * kStage > 76 * 1024 : ST * kStage > 152 * 1024, "shared memory");
   static constexpr int MT = ST >= 4 ? 2 : 1;                 // MMA threads (see there)
   static_assert(COLS * 512 <= ST * kStage, "the sums take the stages' place");
 };
@@ -882,7 +885,7 @@ template <bool GATED, int BN>
 static cudaError_t launch_wide(const Fp8Job& j, const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mu,
                                cudaStream_t stream, DeviceStatus* st) {
   constexpr int smem = (int)sizeof(f8w::Smem<BN>) + 1024, TN = GATED ? 128 : BN;
-  static_assert(smem <= 232448, "shared memory");
+  static_assert(smem <= 232448 && smem > 152 * 1024, "shared memory");  // alone on its SM, which has 512 TMEM columns
   cudaError_t e = set_smem((const void*)fp8_wide_kernel<GATED, BN>, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((j.T + f8w::BM - 1) / f8w::BM) * ((j.N + TN - 1) / TN), pairs = num_sms() / 2;
