@@ -699,6 +699,16 @@ MOBI_API mobi_status mobi_logprobs(const void* logits, int dtype, int64_t T, int
                                    const int64_t* targets, float temperature, int top_k, float* logprob,
                                    float* entropy, float* top_logprob, int32_t* top_index, void* stream);
 
+/*
+ * mobi_fp8_quant, mobi_fp8_gemm, mobi_fp8_gated or mobi_logprobs with the
+ * arguments, the stream included, as n 64-bit words in order: pointers and
+ * integers as they are, a float in its word's first four bytes. For bindings
+ * whose foreign calls cost by the argument. MOBI_ERR_INVALID_ARG if n is not
+ * the call's number of arguments or an int does not fit its type.
+ */
+enum { MOBI_CALL_FP8_QUANT = 0, MOBI_CALL_FP8_GEMM = 1, MOBI_CALL_FP8_GATED = 2, MOBI_CALL_LOGPROBS = 3 };
+MOBI_API mobi_status mobi_call_words(int call, const int64_t* words, int n);
+
 #ifdef __cplusplus
 }
 #endif

@@ -135,3 +135,19 @@ def test_reference_logprobs():
     assert torch.allclose(H, -torch.xlogy(p, p).sum(1))
     assert torch.equal(idx, x.topk(4, 1)[1])
     assert torch.allclose(top, want.gather(1, idx))
+
+
+def test_words_refusals(L):
+    """mobi_call_words: the number of words, the call, ints that do not fit; the rest is refused by the call itself."""
+    import struct
+    q = [0x1000, 1, 4, 128, 128, 1, 0x2000, 128, 0x3000, 0]
+    call = lambda c, w, n=None: L.mobi_call_words(c, struct.pack(f"{len(w)}q", *w), len(w) if n is None else n)  # noqa: E731
+    assert L.mobi_call_words(0, None, 10) == 1
+    assert call(-1, q) == 1 and call(4, q) == 1 and call(0, q, 9) == 1 and call(1, q) == 1 and call(3, q) == 1
+    for i in (1, 5):
+        assert call(0, q[:i] + [q[i] + (1 << 32)] + q[i + 1:]) == 1
+    assert call(0, q[:5] + [64] + q[6:]) == 1 and call(0, q[:8] + [0x3001, 0]) == L.mobi_fp8_quant(
+        0x1000, 1, 4, 128, 128, 1, 0x2000, 128, 0x3001, None)
+    assert call(0, [0, 0, 0, 128, 128, 1, 0, 128, 0, 0]) == 0 and call(1, [0] * 13) == 0 and call(2, [0] * 18) == 0
+    temp = struct.unpack("q", struct.pack("f4x", 1.0))[0]
+    assert call(3, [0, 0, 0, 5, 5, 0, temp, 0, 0, 0, 0, 0, 0]) == 0 and call(3, [0, 0, 0, 5, 5] + [0] * 8) == 1

@@ -14,6 +14,7 @@ ready, by the caller, as for any work queued on another stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -37,6 +38,19 @@ class NormArgs(ctypes.Structure):
                 + [("unit_offset", ctypes.c_int)])
 
 
+_NORM_ARGS = struct.Struct("".join({ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i",
+                                   ctypes.c_float: "f"}[t] for _, t in NormArgs._fields_)).pack
+
+# The other calls' arguments as words of mobi_call_words: one foreign argument
+# instead of 10 to 18, which ctypes converts at 0.1 us each.
+_QUANT, _GEMM, _GATED, _LOGPROBS = range(4)
+_WORDS = {_QUANT: struct.Struct("10q").pack, _GEMM: struct.Struct("13q").pack, _GATED: struct.Struct("18q").pack,
+          _LOGPROBS: struct.Struct("6qf4x6q").pack}
+_NAMES = ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_logprobs", "mobi_norm")
+
+SYMBOLS = _NAMES + ("mobi_call_words",)
+
+
 def bind(L: ctypes.CDLL) -> None:
     """Argument types of the calls of this module."""
     p, i64, ci, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
@@ -45,13 +59,18 @@ def bind(L: ctypes.CDLL) -> None:
     L.mobi_fp8_gated.argtypes = [p, i64, p, i64, i64, p, i64, p, p, i64, p, i64, ci, ci, p, i64, p, p]
     L.mobi_norm.argtypes = [p, p]
     L.mobi_logprobs.argtypes = [p, ci, i64, i64, i64, p, f32, ci, p, p, p, p, p]
-    for n in ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_norm", "mobi_logprobs"):
+    L.mobi_call_words.argtypes = [ci, p, ci]
+    for n in SYMBOLS:
         getattr(L, n).restype = ci
 
 
-SYMBOLS = ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_norm", "mobi_logprobs")
+_lib: list = []
 
-_calls: dict = {}
+
+def _library() -> ctypes.CDLL:
+    from . import lib
+    _lib.append(lib())
+    return _lib[0]
 
 
 def _under(stream, t: torch.Tensor):
@@ -65,47 +84,47 @@ def _under(stream, t: torch.Tensor):
     return torch.cuda.stream(stream)
 
 
-def _call(name: str, device: int, *args) -> None:
-    """Run library call `name` on `device`, its last argument that device's current stream."""
-    fn = _calls.get(name)
-    if fn is None:
-        from . import lib
-        fn = _calls[name] = getattr(lib(), name)
-    if _get_device() != device:
+def _call(call: int, device: int, *words) -> None:
+    """Run a call of mobi_call_words on `device`, on its current stream."""
+    w = _WORDS[call](*words, _raw_stream(device))
+    L = _lib[0] if _lib else _library()
+    if _get_device() == device:
+        status = L.mobi_call_words(call, w, len(w) >> 3)
+    else:
         with torch.cuda.device(device):
-            return _call(name, device, *args)
-    status = fn(*args, _raw_stream(device))
+            status = L.mobi_call_words(call, w, len(w) >> 3)
     if status:
         from . import _check
-        _check(name, status)
+        _check(_NAMES[call], status)
 
 
-def _matrix(t: torch.Tensor, what: str, device=None):
-    """(rows, columns, row pitch) of a CUDA matrix whose rows are contiguous."""
+def _matrix(t: torch.Tensor, what: str, device: int):
+    """(rows, columns, row pitch) of a matrix on CUDA device `device` whose rows are contiguous."""
+    if t.get_device() != device or device < 0:
+        _on(t, what, device)
     if t.dim() != 2:
         raise ValueError(f"{what} must be 2-D")
-    _on(t, what, device)
     (R, C), (ld, sd) = t.shape, t.stride()
-    if C > 1 and sd != 1:
+    if sd != 1 and C > 1:
         raise ValueError(f"the rows of {what} must be contiguous")
-    if R <= 1:
-        ld = max(C, 1) if ld < C else ld
-    elif ld < C:
-        raise ValueError(f"the rows of {what} overlap")
-    return R, C, ld
+    if ld < C:
+        if R > 1:
+            raise ValueError(f"the rows of {what} overlap")
+        ld = C
+    return R, C, ld or 1
 
 
-def _on(t: torch.Tensor, what: str, device=None) -> None:
+def _on(t: torch.Tensor, what: str, device: int | None = None) -> None:
     if not t.is_cuda:
         raise ValueError("libmobi takes CUDA tensors only (no CPU path)")
     if device is not None and t.get_device() != device:
         raise ValueError(f"{what} is on another device")
 
 
-def _vector(t, n: int, what: str, device, dtype=None):
-    """The address of a contiguous vector of n elements (None: no vector)."""
+def _vector(t, n: int, what: str, device, dtype=None) -> int:
+    """The address of a contiguous vector of n elements (None: 0)."""
     if t is None:
-        return None
+        return 0
     _on(t, what, device)
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous vector of {n} elements")
@@ -114,10 +133,11 @@ def _vector(t, n: int, what: str, device, dtype=None):
     return t.data_ptr()
 
 
-def _scales(s: torch.Tensor, kb: int, rb: int, what: str, device) -> int:
-    _on(s, what, device)
+def _scales(s: torch.Tensor, kb: int, rb: int, what: str, device: int) -> int:
+    if s.get_device() != device:
+        _on(s, f"the scale tensor {what}", device)
     if s.dtype is not torch.float32 or s.shape != (kb, rb) or not s.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous fp32 tensor of shape ({kb}, {rb})")
+        raise ValueError(f"the scale tensor {what} must be contiguous fp32 of shape ({kb}, {rb})")
     return s.data_ptr()
 
 
@@ -149,22 +169,23 @@ def mobi_fp8_quant(X: torch.Tensor, block_rows: int = 1, Q: torch.Tensor | None 
     if stream is not None:
         with _under(stream, X):
             return mobi_fp8_quant(X, block_rows, Q, scale)
-    T, K, ldx = _matrix(X, "X")
+    d = X.get_device()
+    T, K, ldx = _matrix(X, "X", d)
     dt = _DT.get(X.dtype, 3)
     if dt == 3:
         raise ValueError("X must be fp32, bf16 or fp16")
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    d, dev = X.get_device(), X.device
+    dev = X.device
     kb, rb = (K + 127) >> 7, T if block_rows == 1 else (T + 127) >> 7
     Q, ldq = _out(Q, T, K, E4M3, "Q", d, dev)
     scale, sp = _new_scales(scale, kb, rb, "scale", d, dev)
-    _call("mobi_fp8_quant", d, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), ldq, sp)
+    _call(_QUANT, d, X.data_ptr(), dt, T, K, ldx, block_rows, Q.data_ptr(), ldq, sp)
     return Q, scale
 
 
-def _operand(Q, scale, what, rows, K, device):
-    """(rows, pitch, codes address, scales address) of an e4m3 operand; rows per scale `rows`."""
+def _operand(Q, scale, what, scale_name, rows, K, device):
+    """(rows, columns, pitch, codes address, scales address) of an e4m3 operand; rows per scale `rows`."""
     if Q.dtype is not E4M3:
         raise ValueError(f"{what} must be e4m3")
     R, k, ld = _matrix(Q, what, device)
@@ -172,7 +193,7 @@ def _operand(Q, scale, what, rows, K, device):
         raise ValueError(f"{what} has {k} columns, X has {K}")
     if R <= 1:
         ld = (ld + 15) & ~15  # one row: the pitch is never used
-    return R, ld, Q.data_ptr(), _scales(scale, (k + 127) >> 7, (R + rows - 1) // rows, f"the scales of {what}", device)
+    return R, k, ld, Q.data_ptr(), _scales(scale, (k + 127) >> 7, (R + rows - 1) // rows, scale_name, device)
 
 
 def mobi_fp8_gemm(X: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, ws: torch.Tensor, out_dtype=torch.float32,
@@ -183,14 +204,13 @@ def mobi_fp8_gemm(X: torch.Tensor, xs: torch.Tensor, W: torch.Tensor, ws: torch.
         with _under(stream, X):
             return mobi_fp8_gemm(X, xs, W, ws, out_dtype, Y)
     d = X.get_device()
-    K = X.shape[-1]
-    T, ldx, xp, xsp = _operand(X, xs, "X", 1, None, None)
-    N, ldw, wp, wsp = _operand(W, ws, "W", 128, K, d)
+    T, K, ldx, xp, xsp = _operand(X, xs, "X", "xs", 1, None, d)
+    N, _, ldw, wp, wsp = _operand(W, ws, "W", "ws", 128, K, d)
     dt = _DT.get(out_dtype, 3)
     if dt == 3:
         raise ValueError("out_dtype must be fp32, bf16 or fp16")
     Y, ldy = _out(Y, T, N, out_dtype, "Y", d, X.device)
-    _call("mobi_fp8_gemm", d, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), ldy)
+    _call(_GEMM, d, xp, ldx, xsp, T, K, wp, ldw, wsp, N, dt, Y.data_ptr(), ldy)
     return Y
 
 
@@ -203,10 +223,9 @@ def mobi_fp8_gated(X: torch.Tensor, xs: torch.Tensor, Wg: torch.Tensor, gs: torc
         with _under(stream, X):
             return mobi_fp8_gated(X, xs, Wg, gs, Wu, us, act, out_dtype, H, hs)
     d, dev = X.get_device(), X.device
-    K = X.shape[-1]
-    T, ldx, xp, xsp = _operand(X, xs, "X", 1, None, None)
-    N, ldg, gp, gsp = _operand(Wg, gs, "Wg", 128, K, d)
-    Nu, ldu, up, usp = _operand(Wu, us, "Wu", 128, K, d)
+    T, K, ldx, xp, xsp = _operand(X, xs, "X", "xs", 1, None, d)
+    N, _, ldg, gp, gsp = _operand(Wg, gs, "Wg", "gs", 128, K, d)
+    Nu, _, ldu, up, usp = _operand(Wu, us, "Wu", "us", 128, K, d)
     if Nu != N:
         raise ValueError("Wg and Wu must have as many rows")
     if act not in _ACT:
@@ -215,11 +234,10 @@ def mobi_fp8_gated(X: torch.Tensor, xs: torch.Tensor, Wg: torch.Tensor, gs: torc
     if dt is None:
         raise ValueError("out_dtype must be fp32, bf16, fp16 or e4m3")
     H, ldh = _out(H, T, N, out_dtype, "H", d, dev)
-    hsp = None
+    hsp = 0
     if dt == 3:
         hs, hsp = _new_scales(hs, (N + 127) >> 7, T, "hs", d, dev)
-    _call("mobi_fp8_gated", d, xp, ldx, xsp, T, K, gp, ldg, gsp, up, ldu, usp, N, _ACT[act], dt, H.data_ptr(),
-          ldh, hsp)
+    _call(_GATED, d, xp, ldx, xsp, T, K, gp, ldg, gsp, up, ldu, usp, N, _ACT[act], dt, H.data_ptr(), ldh, hsp)
     return (H, hs) if dt == 3 else H
 
 
@@ -238,8 +256,8 @@ def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
         with _under(stream, x):
             return mobi_norm(x, weight, bias, eps, kind, block, post, post_weight, post_bias, post_eps, gate, scale,
                              unit_offset, out_dtype, N, n_scale, R)
-    T, D, ldx = _matrix(x, "x")
     d, dev = x.get_device(), x.device
+    T, D, ldx = _matrix(x, "x", d)
     xdt, odt = _DT.get(x.dtype, 3), _DT.get(out_dtype)
     if xdt == 3 or odt is None:
         raise ValueError("x must be fp32, bf16 or fp16, out_dtype one of these or e4m3")
@@ -254,36 +272,43 @@ def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     wdt = 0 if wdt is None else _DT.get(wdt, 3)
     if wdt == 3:
         raise ValueError("the weights and biases must be fp32, bf16 or fp16")
-    a = NormArgs()
-    a.x, a.T, a.D, a.ldx, a.x_dtype, a.weight_dtype, a.out_dtype = x.data_ptr(), T, D, ldx, xdt, wdt, odt
-    a.weight, a.bias = _vector(weight, D, "weight", d), _vector(bias, D, "bias", d)
-    a.kind, a.eps, a.unit_offset = _NORM[kind], eps, int(unit_offset)
+    wp, bp = _vector(weight, D, "weight", d), _vector(bias, D, "bias", d)
+    block_p = gate_p = pwp = pbp = rp = nsp = 0
+    ldb = ldr = gate_st = gate_sd = bdt = gdt = 0
     if block is not None:
         if block.shape != x.shape:
             raise ValueError("block must have the shape of x")
-        a.ldb = _matrix(block, "block", d)[2]
-        a.block, a.block_dtype = block.data_ptr(), _DT.get(block.dtype, 3)
-        if a.block_dtype == 3:
+        ldb = _matrix(block, "block", d)[2]
+        block_p, bdt = block.data_ptr(), _DT.get(block.dtype, 3)
+        if bdt == 3:
             raise ValueError("block must be fp32, bf16 or fp16")
-        a.post, a.post_eps, a.scale = _NORM[post], eps if post_eps is None else post_eps, scale
-        a.post_weight = _vector(post_weight, D, "post_weight", d)
-        a.post_bias = _vector(post_bias, D, "post_bias", d)
+        pwp, pbp = _vector(post_weight, D, "post_weight", d), _vector(post_bias, D, "post_bias", d)
         if gate is not None:
             _on(gate, "gate", d)
-            a.gate_dtype = _DT.get(gate.dtype, 3)
-            if a.gate_dtype == 3:
+            gdt = _DT.get(gate.dtype, 3)
+            if gdt == 3:
                 raise ValueError("gate must be fp32, bf16 or fp16")
-            a.gate_st, a.gate_sd = gate.expand(T, D).stride()
-            a.gate = gate.data_ptr()
-        R, a.ldr = _out(R, T, D, x.dtype, "R", d, dev)
-        a.r_out = R.data_ptr()
+            gate_st, gate_sd = gate.expand(T, D).stride()
+            gate_p = gate.data_ptr()
+        R, ldr = _out(R, T, D, x.dtype, "R", d, dev)
+        rp = R.data_ptr()
     elif R is not None or gate is not None or post_weight is not None or post_bias is not None:
         raise ValueError("R, gate and the post norm's weights need a block")
-    N, a.ldn = _out(N, T, D, out_dtype, "N", d, dev)
-    a.n_out = N.data_ptr()
+    N, ldn = _out(N, T, D, out_dtype, "N", d, dev)
     if odt == 3:
-        n_scale, a.n_scale = _new_scales(n_scale, (D + 127) >> 7, T, "n_scale", d, dev)
-    _call("mobi_norm", d, ctypes.addressof(a))
+        n_scale, nsp = _new_scales(n_scale, (D + 127) >> 7, T, "n_scale", d, dev)
+    a = _NORM_ARGS(x.data_ptr(), block_p, gate_p, wp, bp, pwp, pbp, rp, N.data_ptr(), nsp, T, D, ldx, ldb, ldr, ldn,
+                   gate_st, gate_sd, xdt, bdt, gdt, wdt, odt, _NORM[post], _NORM[kind], eps,
+                   eps if post_eps is None else post_eps, scale, unit_offset)
+    L = _lib[0] if _lib else _library()
+    if _get_device() == d:
+        status = L.mobi_norm(a, _raw_stream(d))
+    else:
+        with torch.cuda.device(d):
+            status = L.mobi_norm(a, _raw_stream(d))
+    if status:
+        from . import _check
+        _check("mobi_norm", status)
     n = (N, n_scale) if odt == 3 else N
     return n if block is None else (n, R)
 
@@ -296,19 +321,18 @@ def mobi_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, tem
     if stream is not None:
         with _under(stream, logits):
             return mobi_logprobs(logits, targets, temperature, top_k, entropy)
-    T, V, ld = _matrix(logits, "logits")
     d, dev = logits.get_device(), logits.device
+    T, V, ld = _matrix(logits, "logits", d)
     dt = _DT.get(logits.dtype, 3)
     if dt == 3:
         raise ValueError("logits must be fp32, bf16 or fp16")
     tp = _vector(targets, T, "targets", d, torch.int64)
     k = int(top_k)
     f32 = torch.float32
-    lp = None if tp is None else torch.empty(T, dtype=f32, device=dev)
+    lp = None if targets is None else torch.empty(T, dtype=f32, device=dev)
     en = torch.empty(T, dtype=f32, device=dev) if entropy else None
     top = torch.empty(T, max(k, 0), dtype=f32, device=dev)
     idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
-    _call("mobi_logprobs", d, logits.data_ptr(), dt, T, V, ld, tp, temperature, k,
-          None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(), top.data_ptr(),
-          idx.data_ptr())
+    _call(_LOGPROBS, d, logits.data_ptr(), dt, T, V, ld, tp, temperature, k, 0 if lp is None else lp.data_ptr(),
+          0 if en is None else en.data_ptr(), top.data_ptr(), idx.data_ptr())
     return lp, en, top, idx

@@ -731,4 +731,32 @@ mobi_status mobi_debug_set_wait_limit(int64_t limit) {
   return MOBI_OK;
 }
 
+mobi_status mobi_call_words(int call, const int64_t* w, int n) {
+  g_last_error[0] = 0;
+  constexpr int kCount[4] = {10, 13, 18, 13};
+  // The words that are ints in each call's argument list.
+  constexpr int kInts[4][2] = {{1, 5}, {9, 9}, {12, 13}, {1, 7}};
+  if (call < MOBI_CALL_FP8_QUANT || call > MOBI_CALL_LOGPROBS || !w || n != kCount[call]) return MOBI_ERR_INVALID_ARG;
+  for (int i : kInts[call])
+    if (w[i] != (int64_t)(int)w[i]) return MOBI_ERR_INVALID_ARG;
+  const auto in = [w](int i) { return reinterpret_cast<const void*>(w[i]); };
+  const auto out = [w](int i) { return reinterpret_cast<void*>(w[i]); };
+  const auto f = [w](int i) { return reinterpret_cast<float*>(w[i]); };
+  switch (call) {
+    case MOBI_CALL_FP8_QUANT:
+      return mobi_fp8_quant(in(0), (int)w[1], w[2], w[3], w[4], (int)w[5], out(6), w[7], f(8), out(9));
+    case MOBI_CALL_FP8_GEMM:
+      return mobi_fp8_gemm(in(0), w[1], f(2), w[3], w[4], in(5), w[6], f(7), w[8], (int)w[9], out(10), w[11], out(12));
+    case MOBI_CALL_FP8_GATED:
+      return mobi_fp8_gated(in(0), w[1], f(2), w[3], w[4], in(5), w[6], f(7), in(8), w[9], f(10), w[11], (int)w[12],
+                            (int)w[13], out(14), w[15], f(16), out(17));
+    default: {
+      float temperature;
+      memcpy(&temperature, &w[6], sizeof temperature);
+      return mobi_logprobs(in(0), (int)w[1], w[2], w[3], w[4], reinterpret_cast<const int64_t*>(w[5]), temperature,
+                           (int)w[7], f(8), f(9), f(10), reinterpret_cast<int32_t*>(w[11]), out(12));
+    }
+  }
+}
+
 }  // extern "C"
