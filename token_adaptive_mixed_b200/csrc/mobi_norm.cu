@@ -312,7 +312,7 @@ constexpr int kMaxD = 16384;  // 512 threads x 4 octets
 //
 // The same steps where every row is 16-byte aligned and D is a multiple of 8,
 // with the types of x and the block known to the compiler and values in pairs.
-// Both kernels are bound by the instructions they issue rather than by memory,
+// Both kernels are bound by issuing (and the barriers between) rather than by memory,
 // this one by a third fewer of them (T = 8192, D = 4096, x, gate and block bf16,
 // norms on both sides, e4m3 out: general 97 us, this one 61.5 us).
 
