@@ -593,3 +593,34 @@ def test_graphs_replayed_at_once(mobi):
     for out, w in zip(outs, want):
         for a, b in zip(out, w):
             assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_rows_far_apart(mobi):
+    """Rows more than 4 GiB apart, read and written: the same as close ones."""
+    g = gen(31)
+    pitch = (1 << 32) + 256  # bytes
+    store = [torch.empty(pitch + 4096, dtype=torch.uint8, device=DEV) for _ in range(2)]
+
+    def far(t, i=0):
+        v = store[i].view(t.dtype).as_strided(t.shape, (pitch // t.element_size(), 1))
+        v.copy_(t)
+        return v
+
+    x = torch.randn(2, 512, generator=g).to(BF16).to(DEV)
+    w = (1 + 0.1 * torch.randn(512, generator=g)).to(BF16).to(DEV)
+    q, s = mobi.mobi_fp8_quant(x)
+    got = mobi.mobi_fp8_quant(far(x), Q=far(torch.zeros_like(q), 1))
+    assert torch.equal(got[0].contiguous().view(torch.uint8), q.view(torch.uint8)) and torch.equal(got[1], s)
+    m, ms = ref.operand(300, 512, 128, g, device=DEV)
+    y = mobi.mobi_fp8_gemm(q, s, m, ms)
+    assert torch.equal(mobi.mobi_fp8_gemm(far(q), s, m, ms, Y=far(torch.zeros_like(y), 1)), y)
+    h = mobi.mobi_fp8_gated(q, s, m, ms, m, ms)
+    assert torch.equal(mobi.mobi_fp8_gated(far(q), s, m, ms, m, ms, H=far(torch.zeros_like(h), 1)), h)
+    n, r = mobi.mobi_norm(far(x), w, block=x, post="rms", scale=0.5, R=far(torch.zeros_like(x), 1))
+    wn, en, wr, er = ref.norm(x, w, None, 1e-6, "rms", block=x, post="rms", scale=0.5)
+    ref.check_close(r, wr, ref.rounded(wr, er, BF16), "r")
+    ref.check_close(n, wn, ref.rounded(wn, en, BF16), "n")
+    t = torch.tensor([3, 500], device=DEV)
+    for a, b in zip(mobi.mobi_logprobs(far(x), t, top_k=5), mobi.mobi_logprobs(x, t, top_k=5)):
+        assert torch.equal(a, b)
+    mobi.mobi_sync_check()

@@ -24,6 +24,7 @@ struct Params {
   mobi_norm_args a;
   int vx, vb, vg, vw, vr, vn;  // rows of x, block, gate, weights, r, n may be accessed 16 bytes at a time
   int tpr;                     // threads of a row
+  uint32_t lx, lb, lr, ln;     // pitches of x, block, r and n in bytes (aligned rows)
 };
 
 // Eight raw elements of ES bytes.
@@ -312,9 +313,10 @@ constexpr int kMaxD = 16384;  // 512 threads x 4 octets
 //
 // The same steps where every row is 16-byte aligned and D is a multiple of 8,
 // with the types of x and the block known to the compiler and values in pairs.
-// Both kernels are bound by issuing (and the barriers between) rather than by memory,
-// this one by a third fewer of them (T = 8192, D = 4096, x, gate and block bf16,
-// norms on both sides, e4m3 out: general 97 us, this one 61.5 us).
+// Both kernels are bound by issuing (and the barriers between) rather than by memory, so
+// options are tested once a row, not once an octet, and addresses are 32-bit products
+// (T = 8192, D = 4096, x, gate and block bf16, norms on both sides, e4m3 out: general 97 us, this
+// one 55.2 us, of which post costs 12 and the gate 4; without both 39 us at 6.0 TB/s).
 
 struct Oct {
   float2 v[4];
@@ -370,9 +372,9 @@ __device__ __forceinline__ Oct load_oct(const void* base, int dtype, int64_t at)
   return r.widen();
 }
 
-__device__ __forceinline__ void store_oct(void* base, int dtype, int64_t at, const Oct& o) {
+__device__ __forceinline__ void store_oct(void* to, int dtype, const Oct& o) {
   if (dtype == MOBI_F32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    float4* q = static_cast<float4*>(to);
     q[0] = make_float4(o.v[0].x, o.v[0].y, o.v[1].x, o.v[1].y);
     q[1] = make_float4(o.v[2].x, o.v[2].y, o.v[3].x, o.v[3].y);
     return;
@@ -388,7 +390,14 @@ __device__ __forceinline__ void store_oct(void* base, int dtype, int64_t at, con
       u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+  *static_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// max(a, |x|, |y|) for a >= 0, NaN if any is.
+__device__ __forceinline__ float max3_abs(float a, float x, float y) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(x), "f"(y));
+  return r;
 }
 
 // Sum over the threads of a row (at most 16 warps); `slot` as in row_sum, its unused entries are zero.
@@ -410,8 +419,8 @@ __device__ __forceinline__ float row_sum16(float v, int tpr, float4* slot) {
 
 template <int NCH>
 __device__ __forceinline__ void norm_octs(Oct (&r)[NCH], int kind, float eps, const void* weight, const void* bias,
-                                          const Params& p, int l, float inv, float4 (*red)[4]) {
-  const int D = (int)p.a.D, tpr = p.tpr;
+                                          const Params& p, uint32_t l, float inv, float4 (*red)[4]) {
+  const uint32_t D = (uint32_t)p.a.D, tpr = p.tpr;
   if (kind == MOBI_NORM_LAYER) {
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -437,21 +446,35 @@ __device__ __forceinline__ void norm_octs(Oct (&r)[NCH], int kind, float eps, co
     rstd.x = rstd.y = root(row_sum16(s.x + s.y, tpr, red[1]) * inv + eps);
   }
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int d = (c * tpr + l) * 8;
-    if (d >= D) break;
+  for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[c].v[i] = __fmul2_rn(r[c].v[i], rstd);
-    if (weight) {
-      Oct w = load_oct(weight, p.a.weight_dtype, d);
+  if (weight) {
+    auto times = [&](Oct& v, Oct w) {
       if (p.a.unit_offset) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w.v[i] = __fadd2_rn(w.v[i], make_float2(1.0f, 1.0f));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[c].v[i] = __fmul2_rn(r[c].v[i], w.v[i]);
+      for (int i = 0; i < 4; ++i) v.v[i] = __fmul2_rn(v.v[i], w.v[i]);
+    };
+    if (p.a.weight_dtype == MOBI_BF16) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const uint32_t d = (c * tpr + l) * 8;
+        if (d < D) times(r[c], load_oct(weight, MOBI_BF16, d));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        if ((c * tpr + l) * 8 < D) times(r[c], load_oct_other(weight, p.a.weight_dtype, (c * tpr + l) * 8));
     }
-    if (bias) {
+  }
+  if (bias) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const uint32_t d = (c * tpr + l) * 8;
+      if (d >= D) break;
       const Oct b = load_oct(bias, p.a.weight_dtype, d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[c].v[i] = __fadd2_rn(r[c].v[i], b.v[i]);
@@ -468,27 +491,33 @@ __global__ void __launch_bounds__(MAXT, MIN) norm_aligned_kernel(const __grid_co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   const mobi_norm_args& a = p.a;
-  const int tpr = p.tpr, D = (int)a.D;
-  const int rows = tpr == 32 ? blockDim.x / 32 : 1;
-  const int64_t stride = (int64_t)gridDim.x * rows;
-  int64_t t = (int64_t)blockIdx.x * rows + (tpr == 32 ? threadIdx.x >> 5 : 0);
-  const int l = tpr == 32 ? (threadIdx.x & 31) : threadIdx.x;
-  if (t >= a.T) return;  // whole warps, and only where a row is one warp
+  const uint32_t tpr = p.tpr, D = (uint32_t)a.D;
+  const uint32_t rows = tpr == 32 ? blockDim.x / 32 : 1;
+  const uint32_t T = (uint32_t)a.T, stride = gridDim.x * rows;
+  uint32_t t = blockIdx.x * rows + (tpr == 32 ? threadIdx.x >> 5 : 0);
+  const uint32_t l = tpr == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  if (t >= T) return;  // whole warps, and only where a row is one warp
   const float inv = 1.0f / (float)D;
   const float2 scale = make_float2(a.scale, a.scale);
 
-  constexpr int XB = XT == MOBI_F32 ? 4 : 2, BB = BT == MOBI_F32 ? 4 : 2;
+  // Row numbers and pitches (bytes) are 32-bit: one multiplication for an address. 64-bit ones took 3 us of
+  // 60 at T = 8192, D = 4096; pointers moved on from row to row spilled (65 us).
+  constexpr uint32_t XB = XT == MOBI_F32 ? 4 : 2, BB = BT == MOBI_F32 ? 4 : 2;
+  const uint32_t nb = a.out_dtype == MOBI_E4M3 ? 1 : (a.out_dtype == MOBI_F32 ? 4 : 2);
+  const auto at = [](const void* base, uint32_t row, uint32_t pitch, uint32_t off) {
+    return const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + (uint64_t)row * pitch + off;
+  };
+
   RawOct<XT> rx[NCH];
   RawOct<BT < 0 ? MOBI_BF16 : BT> rb[NCH];
-  auto fetch = [&](int64_t row) {
-    const uint8_t* px = static_cast<const uint8_t*>(a.x) + row * a.ldx * XB;
-    const uint8_t* pb = BT < 0 ? nullptr : static_cast<const uint8_t*>(a.block) + row * a.ldb * BB;
+  auto fetch = [&](uint32_t row) {
+    const uint8_t* px = at(a.x, row, p.lx, 8 * XB * l);
+    const uint8_t* pb = BT < 0 ? nullptr : at(a.block, row, p.lb, 8 * BB * l);
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int d = (c * tpr + l) * 8;
-      if (d < D) {
-        if constexpr (BT >= 0) rb[c].load(pb + d * BB);
-        rx[c].load(px + d * XB);
+      if ((c * tpr + l) * 8 < D) {
+        if constexpr (BT >= 0) rb[c].load(pb + c * tpr * 8 * BB);
+        rx[c].load(px + c * tpr * 8 * XB);
       } else {
         if constexpr (BT >= 0) rb[c].zero();
         rx[c].zero();
@@ -496,7 +525,7 @@ __global__ void __launch_bounds__(MAXT, MIN) norm_aligned_kernel(const __grid_co
     }
   };
   fetch(t);
-  for (int par = 0; t < a.T; t += stride, par ^= 1) {
+  for (int par = 0; t < T; t += stride, par ^= 1) {
     Oct r[NCH];
     if constexpr (BT >= 0) {
       RawOct<XT> cx[NCH];
@@ -505,66 +534,85 @@ __global__ void __launch_bounds__(MAXT, MIN) norm_aligned_kernel(const __grid_co
         r[c] = rb[c].widen();
         cx[c] = rx[c];
       }
-      if (t + stride < a.T) fetch(t + stride);
+      if (t + stride < T) fetch(t + stride);
       if (a.post != MOBI_NORM_NONE || a.post_weight || a.post_bias)
         norm_octs<NCH>(r, a.post, a.post_eps, a.post_weight, a.post_bias, p, l, inv, red[par]);
+      if (a.gate) {
+        auto times = [](Oct& v, const Oct& g) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v.v[i] = __fmul2_rn(v.v[i], g.v[i]);
+        };
+        const int64_t first = t * a.gate_st;
+        if (a.gate_sd == 0) {  // one value for the row
+          const float f = a.gate_dtype == MOBI_F32    ? static_cast<const float*>(a.gate)[first]
+                          : a.gate_dtype == MOBI_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.gate)[first])
+                                                      : to_f32(static_cast<const __half*>(a.gate)[first]);
+          const float2 f2 = make_float2(f, f);
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            if ((c * tpr + l) * 8 < D) times(r[c], Oct{{f2, f2, f2, f2}});
+        } else if (a.gate_dtype == MOBI_BF16) {
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const uint32_t d = (c * tpr + l) * 8;
+            if (d < D) times(r[c], load_oct(a.gate, MOBI_BF16, first + d));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const uint32_t d = (c * tpr + l) * 8;
+            if (d < D) times(r[c], load_oct_other(a.gate, a.gate_dtype, first + d));
+          }
+        }
+      }
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        const int d = (c * tpr + l) * 8;
+        const uint32_t d = (c * tpr + l) * 8;
         if (d >= D) break;
-        if (a.gate) {
-          Oct g;
-          if (a.gate_sd == 1) {
-            g = load_oct(a.gate, a.gate_dtype, t * a.gate_st + d);
-          } else {  // one value for the row
-            const int64_t at = t * a.gate_st;
-            const float f = a.gate_dtype == MOBI_F32    ? static_cast<const float*>(a.gate)[at]
-                            : a.gate_dtype == MOBI_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.gate)[at])
-                                                        : to_f32(static_cast<const __half*>(a.gate)[at]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g.v[i] = make_float2(f, f);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r[c].v[i] = __fmul2_rn(r[c].v[i], g.v[i]);
-        }
         const Oct x = cx[c].widen();
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[c].v[i] = __ffma2_rn(scale, r[c].v[i], x.v[i]);
-        if (a.r_out) store_oct(a.r_out, XT, t * a.ldr + d, r[c]);
+        if (a.r_out) store_oct(at(a.r_out, t, p.lr, d * XB), XT, r[c]);
       }
     } else {
 #pragma unroll
       for (int c = 0; c < NCH; ++c) r[c] = rx[c].widen();
-      if (t + stride < a.T) fetch(t + stride);
+      if (t + stride < T) fetch(t + stride);
     }
 
     norm_octs<NCH>(r, a.kind, a.eps, a.weight, a.bias, p, l, inv, red[par] + 2);
+    if (a.out_dtype != MOBI_E4M3) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int d = (c * tpr + l) * 8;
-      if (a.out_dtype != MOBI_E4M3) {
-        if (d < D) store_oct(a.n_out, a.out_dtype, t * a.ldn + d, r[c]);
-        continue;
+      for (int c = 0; c < NCH; ++c)
+        if ((c * tpr + l) * 8 < D) store_oct(at(a.n_out, t, p.ln, (c * tpr + l) * 8 * nb), a.out_dtype, r[c]);
+    } else {
+      // All octets' maxima first: one octet's exchanges hide the other's latency.
+      float m[NCH];
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        m[c] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[c] = max3_abs(m[c], r[c].v[i].x, r[c].v[i].y);
+        if ((c * tpr + l) * 8 >= D) m[c] = 0.0f;
       }
-      float m = 0.0f;
-      if (d < D) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, r[c].v[i].x), r[c].v[i].y);
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) m[c] = max_abs(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        if ((c * tpr + l) * 8 >= D) break;
+        const float s = block_scale(__float_as_uint(m[c])), f = __frcp_rn(s);
+        if ((l & 15) == 0) a.n_scale[(uint64_t)((c * tpr + l) >> 4) * T + t] = s;
+        const float2 f2 = make_float2(f, f);
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = __fmul2_rn(r[c].v[i], f2);
+          u[i] = e4m3x2(y.x, y.y);
+        }
+        *reinterpret_cast<uint2*>(at(a.n_out, t, p.ln, (c * tpr + l) * 8)) = make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
       }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (d >= D) continue;
-      const float s = block_scale(__float_as_uint(m)), f = __frcp_rn(s);
-      if ((l & 15) == 0) a.n_scale[(int64_t)(d / 128) * a.T + t] = s;
-      const float2 f2 = make_float2(f, f);
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = __fmul2_rn(r[c].v[i], f2);
-        u[i] = e4m3x2(y.x, y.y);
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.n_out) + t * a.ldn + d) =
-          make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
     }
   }
 }
@@ -589,7 +637,10 @@ static cudaError_t launch_aligned(Params& p, cudaStream_t stream) {
       return launch_dependent(kernel, dim3((unsigned)(need < most ? need : most)), threads, 0, 1, stream, p);
     };
     if (nch == 1) return run(norm_aligned_kernel<XT, BT, 1, 512, 2>, 512, 2);
-    if (nch == 2 && threads <= 256) return run(norm_aligned_kernel<XT, BT, 2, 256, 3>, 256, 3);
+    // Three CTAs to an SM leave 80 registers, which fp32 rows with a block spill from: two (T = 8192, D = 4096,
+    // x and block fp32: 107 us with three, 91 with two; x bf16, block fp32: 68 with three, 79 with two).
+    constexpr int kMin = XT == MOBI_F32 && BT >= 0 ? 2 : 3;
+    if (nch == 2 && threads <= 256) return run(norm_aligned_kernel<XT, BT, 2, 256, kMin>, 256, kMin);
     if (nch == 2) return run(norm_aligned_kernel<XT, BT, 2, 512, 1>, 512, 1);
     return run(norm_aligned_kernel<XT, BT, 4, 512, 1>, 512, 1);
   });
@@ -616,9 +667,21 @@ static cudaError_t launch_types(Params& p, cudaStream_t stream) {
   });
 }
 
+bool plain_type(int t) { return t >= MOBI_F32 && t <= MOBI_F16; }
+int64_t bytes(int t) { return t == MOBI_F32 ? 4 : (t == MOBI_E4M3 ? 1 : 2); }
+bool at(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)a == 0; }
+int wide(const void* p, int64_t ld, int t) { return at(p, 16) && ld * bytes(t) % 16 == 0; }
+
 static cudaError_t launch(Params& p, cudaStream_t stream) {
   const mobi_norm_args& a = p.a;
-  if (a.D % 8 == 0 && p.vx && p.vn && p.vw && (!a.block || p.vb) && (!a.r_out || p.vr) &&
+  const int64_t lx = a.ldx * bytes(a.x_dtype), lb = a.block ? a.ldb * bytes(a.block_dtype) : 0,
+                lr = a.r_out ? a.ldr * bytes(a.x_dtype) : 0, ln = a.ldn * bytes(a.out_dtype);
+  p.lx = (uint32_t)lx;
+  p.lb = (uint32_t)lb;
+  p.lr = (uint32_t)lr;
+  p.ln = (uint32_t)ln;
+  const bool short_rows = ((lx | lb | lr | ln) >> 32) == 0;
+  if (short_rows && a.D % 8 == 0 && p.vx && p.vn && p.vw && (!a.block || p.vb) && (!a.r_out || p.vr) &&
       (!a.gate || a.gate_sd == 0 || (a.gate_sd == 1 && p.vg))) {
     if (a.x_dtype == MOBI_F32) return launch_aligned_x<MOBI_F32>(p, stream);
     if (a.x_dtype == MOBI_BF16) return launch_aligned_x<MOBI_BF16>(p, stream);
@@ -629,11 +692,6 @@ static cudaError_t launch(Params& p, cudaStream_t stream) {
   if (p.a.block_dtype == MOBI_F32) return wide ? launch_types<4, 4>(p, stream) : launch_types<2, 4>(p, stream);
   return wide ? launch_types<4, 2>(p, stream) : launch_types<2, 2>(p, stream);
 }
-
-bool plain_type(int t) { return t >= MOBI_F32 && t <= MOBI_F16; }
-int64_t bytes(int t) { return t == MOBI_F32 ? 4 : (t == MOBI_E4M3 ? 1 : 2); }
-bool at(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)a == 0; }
-int wide(const void* p, int64_t ld, int t) { return at(p, 16) && ld * bytes(t) % 16 == 0; }
 
 }  // namespace nm
 
