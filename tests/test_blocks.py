@@ -151,3 +151,15 @@ def test_words_refusals(L):
     assert call(0, [0, 0, 0, 128, 128, 1, 0, 128, 0, 0]) == 0 and call(1, [0] * 13) == 0 and call(2, [0] * 18) == 0
     temp = struct.unpack("q", struct.pack("f4x", 1.0))[0]
     assert call(3, [0, 0, 0, 5, 5, 0, temp, 0, 0, 0, 0, 0, 0]) == 0 and call(3, [0, 0, 0, 5, 5] + [0] * 8) == 1
+
+
+def test_packed_records_have_their_size():
+    """What the binding hands over in place of arguments is as long as what the C side reads, and says the same."""
+    names = [n for n, _ in blocks.NormArgs._fields_]
+    values = [i + 1 for i in range(len(names))]
+    record = blocks._NORM_ARGS(*values)
+    assert len(record) == ctypes.sizeof(blocks.NormArgs)
+    a = blocks.NormArgs.from_buffer_copy(record)
+    assert [getattr(a, n) for n in names] == values
+    for call, n in ((blocks._QUANT, 10), (blocks._GEMM, 13), (blocks._GATED, 18), (blocks._LOGPROBS, 13)):
+        assert len(blocks._WORDS[call](*range(n))) == 8 * n

@@ -38,8 +38,9 @@ class NormArgs(ctypes.Structure):
                 + [("unit_offset", ctypes.c_int)])
 
 
+# The same record packed in one step. struct pads between fields as C does, but not at the end of a record: "0P" does.
 _NORM_ARGS = struct.Struct("".join({ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i",
-                                   ctypes.c_float: "f"}[t] for _, t in NormArgs._fields_)).pack
+                                   ctypes.c_float: "f"}[t] for _, t in NormArgs._fields_) + "0P").pack
 
 # The other calls' arguments as words of mobi_call_words: one foreign argument
 # instead of 10 to 18, which ctypes converts at 0.1 us each.
