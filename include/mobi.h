@@ -550,8 +550,10 @@ MOBI_API mobi_status mobi_gemm_decode_noalloc(const void* X, int64_t T, int64_t 
  * device-side error word of the current device. Returns MOBI_ERR_TIMEOUT if a
  * bounded wait ran out since the last check (mobi_last_error names the wait
  * site), MOBI_ERR_INVALID_ARG if a decode call met an activation with
- * |x| >= 2^31 (see the activation range above), MOBI_ERR_CUDA on a CUDA error,
- * MOBI_OK otherwise.
+ * |x| >= 2^31 (see the activation range above) or mobi_logprobs a target
+ * outside its vocabulary, MOBI_ERR_CUDA on a CUDA error, MOBI_OK otherwise.
+ * Where several of these happened, mobi_last_error names each of them and the
+ * status is MOBI_ERR_TIMEOUT if a wait was among them.
  */
 MOBI_API mobi_status mobi_sync_check(void* stream);
 

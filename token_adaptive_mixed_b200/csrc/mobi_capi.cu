@@ -711,16 +711,18 @@ mobi_status mobi_sync_check(void* stream) {
   const DeviceStatus zero = {};
   e = cudaMemcpy(dst, &zero, sizeof zero, cudaMemcpyHostToDevice);
   if (e != cudaSuccess) return cuda_status(e);
-  if (h.error & kErrTimeout) {
-    snprintf(g_last_error, sizeof g_last_error, "a bounded wait ran out in a kernel (wait site 0x%x)", h.where);
-    return MOBI_ERR_TIMEOUT;
-  }
-  if (!(h.error & kErrInputRange)) {
-    note_message("a target of mobi_logprobs is outside the vocabulary");
-    return MOBI_ERR_INVALID_ARG;  // kErrTargetRange
-  }
-  note_message("an activation of a decode call (T <= 16) had |x| >= 2^31");
-  return MOBI_ERR_INVALID_ARG;  // kErrInputRange
+  // The whole word was cleared, so the message names every error in it; the status is the timeout's where there is one.
+  char site[80] = "";
+  if (h.error & kErrTimeout)
+    snprintf(site, sizeof site, "a bounded wait ran out in a kernel (wait site 0x%x)", h.where);
+  const char* what[3] = {site,
+                         h.error & kErrInputRange ? "an activation of a decode call (T <= 16) had |x| >= 2^31" : "",
+                         h.error & kErrTargetRange ? "a target of mobi_logprobs is outside the vocabulary" : ""};
+  size_t n = 0;
+  for (const char* m : what)
+    if (*m && n < sizeof g_last_error)
+      n += (size_t)snprintf(g_last_error + n, sizeof g_last_error - n, "%s%s", n ? "; " : "", m);
+  return h.error & kErrTimeout ? MOBI_ERR_TIMEOUT : MOBI_ERR_INVALID_ARG;
 }
 
 mobi_status mobi_debug_set_wait_limit(int64_t limit) {

@@ -27,8 +27,9 @@ struct DeviceStatus {
 
 constexpr uint64_t kDefaultWaitLimit = 1ull << 24;  // seconds of polling: far above any real wait
 
+// Sets an error bit. `where` is kept for the first timeout only, so that another error beside it cannot rename its site.
 __device__ __forceinline__ void report_error(DeviceStatus* st, uint32_t bit, uint32_t where) {
-  if ((atomicOr(&st->error, bit) & bit) == 0) st->where = where;
+  if ((atomicOr(&st->error, bit) & bit) == 0 && bit == kErrTimeout) st->where = where;
 }
 
 // ---- mbarrier ---------------------------------------------------------------
