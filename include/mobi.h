@@ -667,8 +667,10 @@ typedef struct mobi_norm_args {
  * x, block, gate and the weights are MOBI_F32, MOBI_BF16 or MOBI_F16; n also
  * MOBI_E4M3. Every pointer is aligned to its element (16-byte aligned rows are read and
  * written faster). T = 0: nothing. D from 1 to 16384 (MOBI_ERR_UNSUPPORTED_SHAPE beyond),
- * T <= 2^28; pitches >= D; eps, post_eps >= 0 and scale finite. Squares are summed in fp32: rows with values
- * beyond about 1e18 overflow to a norm of 0, and a zero row needs eps > 0. Outputs do not overlap the inputs or each
+ * T <= 2^28; pitches >= D; eps, post_eps >= 0 and scale finite. A norm's sum of squares (LAYER: of the differences
+ * from the mean) is held in fp32 unscaled: a row whose root mean square passes 1.8e19 / sqrt(D) (1.4e17 at D = 16384)
+ * overflows it and is normed to 0 (before the bias), and with eps = 0 the root mean square has to be above 1e-18 (a zero
+ * row then gives NaN). Outputs do not overlap the inputs or each
  * other, except r_out = x with the same pitch.
  */
 MOBI_API mobi_status mobi_norm(const mobi_norm_args* args, void* stream);

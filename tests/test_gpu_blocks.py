@@ -624,3 +624,31 @@ def test_rows_far_apart(mobi):
     for a, b in zip(mobi.mobi_logprobs(far(x), t, top_k=5), mobi.mobi_logprobs(x, t, top_k=5)):
         assert torch.equal(a, b)
     mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("D", [4096, 4095, 16384, 16383])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_range_of_the_squares(mobi, D, kind):
+    """Rows on both sides of the stated limit of the sum of squares, 1.8e19 / sqrt(D), before and after the residual
+    sum; rows just above the smallest root mean square where eps is 0."""
+    sign = (torch.arange(D) % 2 * -2 + 1).float()
+    limit = math.sqrt(torch.finfo(torch.float32).max) / math.sqrt(D)
+    x = torch.stack([0.97 * limit * sign, 1.03 * limit * sign, 3.0 * sign]).to(DEV)
+    y = mobi.mobi_norm(x, kind=kind, out_dtype=F32)
+    n, en, _, _ = ref.norm(x, None, None, 1e-6, kind)
+    ref.check_close(y[[0, 2]], n[[0, 2]], ref.rounded(n, en, F32)[[0, 2]])
+    assert (y[1] == 0).all()
+    q, s = mobi.mobi_norm(x, kind=kind, out_dtype=E4M3)
+    ref.check_quantised(q[[0, 2]], s[:, [0, 2]], n[[0, 2]], en[[0, 2]])
+    assert (q[1].float() == 0).all() and (s[:, 1] == 2.0 ** -126).all()
+    base = torch.randn(3, D, generator=gen(D)).to(DEV)
+    case = dict(x=base, weight=None, bias=None, eps=1e-6, kind="rms", block=x, post=kind, post_eps=1e-6)
+    y, r = mobi.mobi_norm(out_dtype=F32, **case)
+    n, en, wr, er = ref.norm(**case)
+    for got, want, err in ((y, n, en), (r, wr, er)):
+        ref.check_close(got[[0, 2]], want[[0, 2]], ref.rounded(want, err, F32)[[0, 2]])
+    assert torch.equal(r[1], base[1])
+    small = 1e-18 * sign[None].to(DEV)
+    n, en, _, _ = ref.norm(small, None, None, 0.0, kind)
+    ref.check_close(mobi.mobi_norm(small, kind=kind, eps=0.0, out_dtype=F32), n, ref.rounded(n, en, F32))
+    assert torch.isnan(mobi.mobi_norm(torch.zeros(1, D, device=DEV), kind=kind, eps=0.0, out_dtype=F32)).all()
