@@ -43,12 +43,15 @@
  *   - Every pointer argument is a DEVICE pointer (allocated by the caller, e.g.
  *     through PyTorch), unless stated otherwise. The library never allocates or
  *     frees device memory; all scratch memory comes from the caller's `ws`.
- *   - Every pointer must be 16-byte aligned (128-bit vector accesses).
+ *   - Every pointer must be 16-byte aligned (128-bit vector accesses); the
+ *     calls beside the mixed-bit layer (mobi_fp8_*, mobi_norm, mobi_logprobs)
+ *     say at each what they ask of pointers and pitches, mostly less.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Calls enqueue work and return without synchronising.
  *   - Arguments are validated on the host before anything is launched; on an
  *     error nothing is enqueued and the status says why.
- *   - Supported shapes: S in {1,2,3,4} slices of b = 2 bits (or b = 1 bit
+ *   - Supported shapes of the mixed-bit layer (the other calls give theirs): S
+ *     in {1,2,3,4} slices of b = 2 bits (or b = 1 bit
  *     through mobi_pack_bits), group G = 128 along K (256 or 512 through
  *     mobi_pack_bits), K % 128 == 0, N % 16 == 0, T >= 0. K, N, T up to 2^30 elements per
  *     dimension and N*K, T*K, T*N below 2^40.
@@ -120,7 +123,7 @@ typedef enum {
   MOBI_OK = 0,
   MOBI_ERR_INVALID_ARG = 1,       /* null pointer, negative size, S/G out of range */
   MOBI_ERR_UNSUPPORTED_SHAPE = 2, /* K % 128, N % 16, or sizes beyond the limits */
-  MOBI_ERR_MISALIGNED = 3,        /* a pointer is not 16-byte aligned */
+  MOBI_ERR_MISALIGNED = 3,        /* a pointer or pitch is not aligned as the call asks */
   MOBI_ERR_WORKSPACE = 4,         /* ws == NULL or ws_bytes below the required size */
   MOBI_ERR_CUDA = 5,              /* a CUDA launch or query failed (error cleared) */
   MOBI_ERR_TIMEOUT = 6,           /* a device-side bounded wait ran out */
