@@ -716,6 +716,18 @@ MOBI_API mobi_status mobi_logprobs(const void* logits, int dtype, int64_t T, int
 enum { MOBI_CALL_FP8_QUANT = 0, MOBI_CALL_FP8_GEMM = 1, MOBI_CALL_FP8_GATED = 2, MOBI_CALL_LOGPROBS = 3 };
 MOBI_API mobi_status mobi_call_words(int call, const int64_t* words, int n);
 
+/*
+ * How mobi_fp8_gemm (gated 0) or mobi_fp8_gated (1) divides a call of these
+ * sizes on a device of `sms` multiprocessors, without launching anything:
+ *   plan[0]  1: the wide kernel (tokens on the lanes), 0: the narrow one
+ *   plan[1]  weight rows (wide) or tokens (narrow) of a tile
+ *   plan[2]  CTAs that share a tile
+ *   plan[3]  tiles
+ *   plan[4]  tiles that one of them takes in a row, at most
+ * Test use only. T, N, K >= 1 and sms >= 2 (MOBI_ERR_INVALID_ARG).
+ */
+MOBI_API mobi_status mobi_debug_fp8_plan(int64_t T, int64_t N, int64_t K, int gated, int sms, int64_t plan[5]);
+
 #ifdef __cplusplus
 }
 #endif

@@ -163,3 +163,46 @@ def test_packed_records_have_their_size():
     assert [getattr(a, n) for n in names] == values
     for call, n in ((blocks._QUANT, 10), (blocks._GEMM, 13), (blocks._GATED, 18), (blocks._LOGPROBS, 13)):
         assert len(blocks._WORDS[call](*range(n))) == 8 * n
+
+
+def _plan(L, T, N, K, gated, sms=148):
+    p = (ctypes.c_int64 * 5)()
+    assert L.mobi_debug_fp8_plan(T, N, K, gated, sms, p) == 0
+    return tuple(p)
+
+
+def test_plan_refusals(L):
+    p = (ctypes.c_int64 * 5)()
+    call = lambda T=4, N=4, K=4, g=0, sms=148, q=p: L.mobi_debug_fp8_plan(T, N, K, g, sms, q)  # noqa: E731
+    assert call() == 0
+    assert call(T=0) == 1 and call(N=0) == 1 and call(K=0) == 1 and call(g=2) == 1 and call(sms=1) == 1
+    assert call(q=None) == 1 and call(T=1 << 29) == 2
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+def test_every_plan_has_a_gpu_test(L, gated):
+    """Whatever kernel, tile and cluster a size can be given, a size of the GPU tests is given it too, and the wide
+    kernel's tests have pairs that take three tiles in a row or more."""
+    import test_gpu_blocks as gpu
+    tested = {_plan(L, *s, gated)[:3] for s in (gpu.PLANS_GATED if gated else gpu.PLANS)}
+    steps = lambda top: sorted({round(2 ** (i / 4)) for i in range(4 * top)})  # noqa: E731
+    reached = {_plan(L, T, N, K, gated)[:3] for T in steps(13) for N in steps(15) for K in steps(14)}
+    assert reached <= tested, reached - tested
+    most = {}
+    for s in gpu.PLANS_GATED if gated else gpu.PLANS:
+        p = _plan(L, *s, gated)
+        most[p[:2]] = max(most.get(p[:2], 0), p[4])
+    assert all(most[w] >= 3 for w in ([(1, 256)] if gated else [(1, 128), (1, 256)])), most
+
+
+def test_plan_covers_the_output(L):
+    """Tiles times their size reach every output, and the cluster divides no K below one block for each CTA."""
+    for gated in (0, 1):
+        for T in (1, 17, 64, 129, 333, 5000):
+            for N in (1, 128, 4099, 28672):
+                for K in (1, 300, 4096):
+                    wide, cols, share, tiles, row = _plan(L, T, N, K, gated)
+                    tt, tn = (256, 128 if gated else cols) if wide else (cols, 128)
+                    assert tiles == -(-T // tt) * -(-N // tn)
+                    assert row == (-(-tiles // 74) if wide else 1)
+                    assert share == 2 if wide else 1 <= share <= max(1, -(-K // 128) // 2)

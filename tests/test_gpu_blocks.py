@@ -70,7 +70,7 @@ def test_quant_edges(mobi, rows):
 
 # ---- products -------------------------------------------------------------------------------
 
-# Both kernels, every token tile, every split of K (one block to eight CTAs), ragged K, odd N and T.
+# Both kernels, one block of K to eight CTAs, ragged K, odd N and T (every kernel, tile and cluster: PLANS below).
 GEMM = [(1, 128, 128), (1, 1, 16), (1, 4096, 4096), (2, 300, 1000), (16, 129, 2048), (17, 640, 272), (32, 77, 1536),
         (33, 500, 640), (64, 1024, 512), (65, 200, 128), (128, 257, 1040), (129, 384, 3200), (200, 4096, 1024),
         (256, 256, 128), (333, 4099, 512), (1000, 1500, 384), (2049, 513, 272), (37, 9000, 144), (100, 16, 8192)]
@@ -652,3 +652,154 @@ def test_norm_range_of_the_squares(mobi, D, kind):
     n, en, _, _ = ref.norm(small, None, None, 0.0, kind)
     ref.check_close(mobi.mobi_norm(small, kind=kind, eps=0.0, out_dtype=F32), n, ref.rounded(n, en, F32))
     assert torch.isnan(mobi.mobi_norm(torch.zeros(1, D, device=DEV), kind=kind, eps=0.0, out_dtype=F32)).all()
+
+
+# ---- every division of a product -------------------------------------------------------------
+
+# One call or more for each kernel, tile and cluster that a call of any size can be given (test_blocks.py holds the
+# lists against the library's own choice), with odd sizes and ragged blocks of K; the last ones of each list are the
+# wide kernel's: one tile, then two to five tiles that a pair takes in a row, ragged at both ends.
+PLANS = [(1, 1, 1), (3, 200, 386), (5, 77, 642), (9, 333, 901), (2, 1000, 1154), (13, 141, 1409), (16, 300, 1665),
+         (1, 500, 1923), (17, 45, 100), (21, 99, 385), (25, 207, 647), (31, 130, 899), (32, 300, 1179),
+         (19, 400, 1413), (27, 151, 1665), (30, 260, 1969), (34, 9551, 1126), (40, 8822, 2966), (35, 6482, 2195),
+         (37, 5518, 2148), (57, 300, 1665), (64, 190, 1925), (38, 13777, 2435), (38, 19484, 2041), (73, 3660, 2948),
+         (258, 1084, 2959), (92, 1956, 2422), (131, 907, 2400), (99, 230, 2064), (140, 130, 2088), (69, 300, 1683),
+         (130, 150, 1667), (80, 140, 1926), (133, 270, 1988), (333, 700, 270), (600, 4099, 1024), (1000, 8200, 2050),
+         (2049, 4099, 640), (2100, 2993, 1040), (4096, 4099, 1040), (4097, 8192, 144)]
+PLANS_GATED = [(1, 1, 1), (3, 200, 386), (5, 77, 642), (9, 333, 901), (2, 1000, 1154), (13, 141, 1409), (16, 300, 1665),
+               (1, 500, 1923), (17, 45, 100), (21, 99, 385), (25, 207, 647), (31, 130, 899), (32, 300, 1179),
+               (19, 400, 1413), (27, 151, 1665), (30, 260, 1969), (38, 11822, 1136), (35, 7007, 2458), (281, 1359, 2758),
+               (48, 150, 1034), (66, 140, 1034), (37, 300, 903), (100, 200, 901), (33, 140, 1163), (65, 260, 1163),
+               (50, 300, 1419), (127, 200, 1438), (38, 131, 1665), (70, 300, 1689), (64, 260, 1940), (70, 140, 1921),
+               (77, 500, 300), (2100, 1300, 400), (1000, 5000, 1040), (2100, 2993, 1040), (2049, 4099, 272)]
+
+
+def guarded(T, N, dtype, off):
+    """A matrix [T, N] whose rows start `off` elements into rows of a larger tensor full of 7, and a check of the rest."""
+    buf = torch.full((T + 2, (N + 15) // 16 * 16 + 32), 7.0, device=DEV).to(dtype)
+    kept = buf.clone()
+
+    def check():
+        raw, want = buf.view(torch.uint8), kept.view(torch.uint8)
+        at = slice(off * buf.element_size(), (off + N) * buf.element_size())
+        raw[1:T + 1, at] = want[1:T + 1, at]
+        assert torch.equal(raw, want), "written outside the output"
+    return buf[1:T + 1, off:off + N], check
+
+
+@pytest.mark.parametrize("T,N,K", PLANS)
+def test_gemm_every_plan(mobi, T, N, K):
+    g = gen(T + 31 * N + K)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, 0.02, device=DEV)
+    x, w = _pitched(x), _pitched(w)
+    want, err = ref.product(x, xs, w, ws)
+    for dtype, off in ((F32, 16), (BF16, 16), (F16, 3), (F32, 1)):  # rows at multiples of 16 bytes, and others
+        y, check = guarded(T, N, dtype, off)
+        mobi.mobi_fp8_gemm(x, xs, w, ws, out_dtype=dtype, Y=y)
+        mobi.mobi_sync_check()
+        ref.check_close(y, want, ref.rounded(want, err, dtype), f"{dtype}")
+        check()
+    again = mobi.mobi_fp8_gemm(x, xs, w, ws)
+    assert all(torch.equal(mobi.mobi_fp8_gemm(x, xs, w, ws), again) for _ in range(3))
+
+
+@pytest.mark.parametrize("T,N,K", PLANS_GATED)
+def test_gated_every_plan(mobi, T, N, K):
+    g = gen(T + 37 * N + K)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    wg, gs = ref.operand(N, K, 128, g, 0.05, device=DEV)
+    wu, us = ref.operand(N, K, 128, g, 0.05, device=DEV)
+    x, wg, wu = _pitched(x), _pitched(wg), _pitched(wu)
+    for act in (("silu", "gelu"), ("relu", "gelu_tanh"))[(T + N) % 2]:
+        h, err = ref.gated(x, xs, wg, gs, wu, us, act)
+        for dtype, off in ((F32, 16), (BF16, 16), (F16, 3)):
+            y, check = guarded(T, N, dtype, off)
+            mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, act=act, out_dtype=dtype, H=y)
+            mobi.mobi_sync_check()
+            ref.check_close(y, h, ref.rounded(h, err, dtype), f"{dtype}")
+            check()
+        for off in (16, 5):
+            q, check = guarded(T, N, E4M3, off)
+            scales = torch.full(((N + 127) // 128, T), 7.0, device=DEV)
+            mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, act=act, out_dtype=E4M3, H=q, hs=scales)
+            mobi.mobi_sync_check()
+            ref.check_quantised(q, scales, h, err)
+            check()
+    first = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, out_dtype=E4M3)
+    for _ in range(3):
+        q, s = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, out_dtype=E4M3)
+        assert torch.equal(q.view(torch.uint8), first[0].view(torch.uint8)) and torch.equal(s, first[1])
+
+
+@pytest.mark.parametrize("T,N,K", [(2049, 4099, 640), (4096, 4099, 1040)])
+def test_tiles_in_a_row_single_blocks(mobi, T, N, K):
+    """Every tile that a pair takes after its first uses its own rows' scales and each block of K counts: all blocks but
+    one are zero, and the scales differ by powers of two from tile to tile."""
+    g = gen(T)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, device=DEV)
+    xs *= torch.exp2((torch.arange(T, device=DEV) // 128 % 7 - 3).float())[None]
+    ws *= torch.exp2((torch.arange(ws.shape[1], device=DEV) % 5 - 2).float())[None]
+    last = (K - 1) // 128
+    for b in (0, 2, last):
+        xb = torch.zeros_like(x)
+        xb[:, 128 * b:128 * b + 128] = x[:, 128 * b:128 * b + 128]
+        want, err = ref.product(xb, xs, w, ws)
+        ref.check_close(mobi.mobi_fp8_gemm(xb, xs, w, ws), want, ref.rounded(want, err, F32))
+    mobi.mobi_sync_check()
+
+
+def test_tiles_in_a_row_beside_another_call(mobi):
+    """Calls whose pairs take several tiles, on two streams at once and captured into a graph: the bits of a call alone."""
+    g = gen(17)
+    x, xs = ref.operand(2100, 1040, 1, g, device=DEV)
+    w, ws = ref.operand(2993, 1040, 128, g, 0.05, device=DEV)
+    u, us = ref.operand(2993, 1040, 128, g, 0.05, device=DEV)
+    y, (h, hs) = mobi.mobi_fp8_gemm(x, xs, w, ws), mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = (mobi.mobi_fp8_gemm(x, xs, w, ws), *mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3))
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    outs = []
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            p = mobi.mobi_fp8_gemm(x, xs, w, ws)
+        with torch.cuda.stream(b):
+            q = mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3)
+        with torch.cuda.stream(c):
+            graph.replay()
+        outs.append((p, *q))
+    torch.cuda.synchronize()
+    mobi.mobi_sync_check()
+    for out in outs + [held]:
+        for got, want in zip(out, (y, h, hs)):
+            assert torch.equal(got.contiguous().view(torch.uint8), want.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,N,K", [(2100, 2993, 1040), (4096, 4099, 1040)])
+def test_timeout_with_tiles_in_a_row(mobi, T, N, K):
+    """A wait that runs out before the first of several tiles ends the kernel with an error status."""
+    g = gen(T)
+    x, xs = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, 0.05, device=DEV)
+    u, us = ref.operand(N, K, 128, g, 0.05, device=DEV)
+    want, err = ref.product(x, xs, w, ws)
+    h, eh = ref.gated(x, xs, w, ws, u, us, "silu")
+    mobi.mobi_sync_check()
+    for call in (lambda: mobi.mobi_fp8_gemm(x, xs, w, ws), lambda: mobi.mobi_fp8_gated(x, xs, w, ws, u, us),
+                 lambda: mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3)):
+        mobi.mobi_debug_set_wait_limit(1)
+        try:
+            call()
+            with pytest.raises(mobi.MobiError) as e:
+                mobi.mobi_sync_check()
+            assert e.value.status == 6  # MOBI_ERR_TIMEOUT
+        finally:
+            mobi.mobi_debug_set_wait_limit(0)
+        mobi.mobi_sync_check()
+    ref.check_close(mobi.mobi_fp8_gemm(x, xs, w, ws), want, ref.rounded(want, err, F32))
+    q, s = mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3)
+    ref.check_quantised(q, s, h, eh)
+    mobi.mobi_sync_check()

@@ -49,7 +49,7 @@ _WORDS = {_QUANT: struct.Struct("10q").pack, _GEMM: struct.Struct("13q").pack, _
           _LOGPROBS: struct.Struct("6qf4x6q").pack}
 _NAMES = ("mobi_fp8_quant", "mobi_fp8_gemm", "mobi_fp8_gated", "mobi_logprobs", "mobi_norm")
 
-SYMBOLS = _NAMES + ("mobi_call_words",)
+SYMBOLS = _NAMES + ("mobi_call_words", "mobi_debug_fp8_plan")
 
 
 def bind(L: ctypes.CDLL) -> None:
@@ -61,6 +61,7 @@ def bind(L: ctypes.CDLL) -> None:
     L.mobi_norm.argtypes = [p, p]
     L.mobi_logprobs.argtypes = [p, ci, i64, i64, i64, p, f32, ci, p, p, p, p, p]
     L.mobi_call_words.argtypes = [ci, p, ci]
+    L.mobi_debug_fp8_plan.argtypes = [i64, i64, i64, ci, ci, p]
     for n in SYMBOLS:
         getattr(L, n).restype = ci
 

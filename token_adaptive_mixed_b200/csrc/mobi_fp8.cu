@@ -992,4 +992,18 @@ mobi_status mobi_fp8_gated(const void* X, int64_t ldx, const float* xs, int64_t 
   return status_of(launch_fp8<true>(j, static_cast<cudaStream_t>(stream)));
 }
 
+mobi_status mobi_debug_fp8_plan(int64_t T, int64_t N, int64_t K, int gated, int sms, int64_t plan[5]) {
+  clear_message();
+  if (T < 1 || N < 1 || K < 1 || gated < 0 || gated > 1 || sms < 2 || !plan) return MOBI_ERR_INVALID_ARG;
+  if (T > kMaxDim || N > kMaxDim || K > kMaxDim) return MOBI_ERR_UNSUPPORTED_SHAPE;
+  const Fp8Plan p = fp8_plan(T, N, K, gated != 0, sms);
+  const int64_t tt = p.wide ? f8w::BM : p.bn, tn = p.wide && !gated ? p.bn : 128;  // tokens and outputs of a tile
+  plan[0] = p.wide;
+  plan[1] = p.bn;
+  plan[2] = p.wide ? 2 : p.csize;
+  plan[3] = ((T + tt - 1) / tt) * ((N + tn - 1) / tn);
+  plan[4] = p.wide ? (plan[3] + sms / 2 - 1) / (sms / 2) : 1;
+  return MOBI_OK;
+}
+
 }  // extern "C"
