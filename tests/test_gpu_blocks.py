@@ -803,3 +803,57 @@ def test_timeout_with_tiles_in_a_row(mobi, T, N, K):
     q, s = mobi.mobi_fp8_gated(x, xs, w, ws, u, us, out_dtype=E4M3)
     ref.check_quantised(q, s, h, eh)
     mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("D,off", [(520, 0), (521, 0), (520, 3), (4096, 0), (4097, 0), (97, 0), (9000, 0), (9001, 0)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("where", ["x", "block", "gate", "post"])
+def test_norm_rows_that_are_not_finite(mobi, D, off, kind, where):
+    """Infinities and NaN in some rows, from every input: those rows follow the definition (NaN where it gives NaN, 0
+    where an infinite sum of squares leaves 0, and the scales and codes of their blocks), all others keep their bounds.
+    With more rows than CTAs, so that a row follows a bad one in the same threads; both kernels (odd D, odd starts)."""
+    T, inf, nan = 1500, float("inf"), float("nan")
+    g = gen(D + off)
+    bad = {1: inf, 2: nan, 4: -inf, 700: nan, 701: inf, 1498: inf}
+    wide = lambda t: torch.cat([t.new_zeros(T, off), t], 1).to(DEV)[:, off:]  # noqa: E731
+    base = torch.randn(T, D, generator=g) * 2
+    base[0], base[3] = 0.0, 2.5
+    block, gate = torch.randn(T, D, generator=g), torch.randn(T, D, generator=g) * 0.5 + 1.5
+    block[0] = block[3] = 0.0
+    at = {"x": base, "block": block, "gate": gate, "post": block}[where]
+    for t, v in bad.items():
+        at[t, (t * 7) % D] = v
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(DEV)
+    case = dict(x=wide(base), weight=w, bias=None, eps=1e-6, kind=kind)
+    if where != "x":
+        case.update(block=wide(block), gate=wide(gate), post="rms" if where == "post" else "none", post_eps=1e-5, scale=0.5)
+    n, en, r, er = ref.norm(**case)
+    good = torch.ones(T, dtype=torch.bool, device=DEV)
+    good[list(bad)] = False
+    assert torch.isfinite(n[good]).all() and torch.isnan(n[~good]).any(1).all()
+    assert ((n == 0) | torch.isnan(n))[~good].all()
+
+    def same(got, want, bound, dtype, what):
+        got = got.double()
+        ref.check_close(got[good], want[good], ref.rounded(want, bound, dtype)[good], what)
+        assert torch.equal(torch.isnan(got[~good]), torch.isnan(want[~good])), what
+        return got[~good], want[~good]
+
+    for dtype in (F32, BF16):
+        y = mobi.mobi_norm(out_dtype=dtype, **case)
+        if where != "x":
+            y, rr = y
+            a, b = same(rr, r, er, F32, "r")
+            assert torch.equal(torch.isinf(a), torch.isinf(b)) and torch.equal(a[torch.isinf(b)], b[torch.isinf(b)])
+        a, b = same(y, n, en, dtype, "n")
+        assert torch.equal(a.nan_to_num(1.0), b.nan_to_num(1.0))
+    y = mobi.mobi_norm(out_dtype=E4M3, **case)
+    q, s = y if where == "x" else y[0]
+    ref.check_quantised(q[good], s[:, good], n[good], en[good], "codes")
+    broken = torch.isnan(ref.blocks(n[~good], 1)).any(3)[:, 0]  # [rows, blocks]
+    assert torch.equal(torch.isnan(s[:, ~good].t()), broken) and (s[:, ~good].t()[~broken] == 2.0 ** -126).all()
+    v = ref.blocks(q[~good].float(), 1)[:, 0]
+    inside = (torch.arange(v[0].numel(), device=DEV) < D).view(v[0].shape)
+    for i in range(len(bad)):
+        assert torch.isnan(v[i][broken[i]][inside[broken[i]]]).all() and (v[i][~broken[i]] == 0).all()
+    mobi.mobi_sync_check()
