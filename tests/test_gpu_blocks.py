@@ -857,3 +857,20 @@ def test_norm_rows_that_are_not_finite(mobi, D, off, kind, where):
     for i in range(len(bad)):
         assert torch.isnan(v[i][broken[i]][inside[broken[i]]]).all() and (v[i][~broken[i]] == 0).all()
     mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("T,D", [(5, 264), (600, 2048), (600, 264), (5, 4104), (5, 8200), (5, 1001), (600, 4097), (5, 8201)])
+@pytest.mark.parametrize("xd", [F32, BF16, F16])
+@pytest.mark.parametrize("bd", [None, F32, BF16, F16])
+def test_norm_types(mobi, T, D, xd, bd):
+    """Each type of x with each of the block, the weights and the gate, and each shape of the gate, in every form of both
+    kernels (one, two and four octets of a thread, few rows and many)."""
+    g = gen(T + D)
+    outs = [BF16, E4M3, F32, F16]
+    for i, wd in enumerate((F32, BF16, F16)):
+        for j, gate in enumerate(("channel", "token", "full") if bd is not None else ("none",)):
+            case = norm_case(T, D, xd, bd, wd, "none", ("rms", "layer", "none")[(i + j) % 3], ("layer", "rms")[j % 2], g, F32)
+            if bd is not None:
+                shape = {"channel": (D,), "token": (T, 1), "full": (T, D)}[gate]
+                case["gate"] = torch.randn(*shape, generator=g).to((F32, F16, BF16)[(i + 2 * j) % 3]).to(DEV)
+            check_norm(mobi, case, outs[(i + j + (bd is None)) % 4])
