@@ -206,3 +206,17 @@ def test_plan_covers_the_output(L):
                     assert tiles == -(-T // tt) * -(-N // tn)
                     assert row == (-(-tiles // 74) if wide else 1)
                     assert share == 2 if wide else 1 <= share <= max(1, -(-K // 128) // 2)
+
+
+def test_gradients_are_refused():
+    """No call has a backward pass: a tensor that requires a gradient is refused where gradients are recorded (before
+    anything else is looked at, so also here), and taken under no_grad (here: refused as a CPU tensor)."""
+    x = torch.zeros(4, 128, requires_grad=True)
+    q, s = torch.zeros(4, 128).to(torch.float8_e4m3fn), torch.ones(1, 4, requires_grad=True)
+    for f in (lambda: mobi.mobi_fp8_quant(x), lambda: mobi.mobi_norm(x), lambda: mobi.mobi_logprobs(x),
+              lambda: blocks._vector(x[0], 128, "weight", 0), lambda: blocks._scales(s, 1, 4, "xs", 0),
+              lambda: blocks._out(x, 4, 128, torch.float32, "Y", 0, x.device)):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            f()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensors only"):
+            f()

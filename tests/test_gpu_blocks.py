@@ -874,3 +874,28 @@ def test_norm_types(mobi, T, D, xd, bd):
                 shape = {"channel": (D,), "token": (T, 1), "full": (T, D)}[gate]
                 case["gate"] = torch.randn(*shape, generator=g).to((F32, F16, BF16)[(i + 2 * j) % 3]).to(DEV)
             check_norm(mobi, case, outs[(i + j + (bd is None)) % 4])
+
+
+def test_gradients_are_refused(mobi):
+    """Each input in turn requires a gradient: refused where gradients are recorded, the same bits under no_grad."""
+    x, b, g = torch.randn(4, 256, device=DEV), torch.randn(4, 256, device=DEV), torch.randn(4, 1, device=DEV)
+    v = [torch.randn(256, device=DEV) for _ in range(4)]
+    q, s = mobi.mobi_fp8_quant(x)
+    w, ws = mobi.mobi_fp8_quant(x, block_rows=128)
+    norm = lambda x, b, g, w, c, p, d: mobi.mobi_norm(x, w, c, block=b, gate=g, post="rms", post_weight=p,  # noqa: E731
+                                                      post_bias=d)
+    calls = [(lambda x: mobi.mobi_fp8_quant(x), [x]), (lambda x: mobi.mobi_logprobs(x, top_k=2), [x]),
+             (lambda s, ws: mobi.mobi_fp8_gemm(q, s, w, ws), [s, ws]),
+             (lambda s, gs, us: mobi.mobi_fp8_gated(q, s, w, gs, w, us), [s, ws, ws.clone()]), (norm, [x, b, g, *v])]
+    flat = lambda o: [t for t in (o if isinstance(o, tuple) else (o,)) if t is not None]  # noqa: E731
+    for call, args in calls:
+        want = flat(call(*args))
+        for i in range(len(args)):
+            some = [a.clone().requires_grad_(i == j) for j, a in enumerate(args)]
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(*some)
+            with torch.no_grad():
+                got = flat(call(*some))
+            for a, e in zip(got, want):
+                assert torch.equal(a.view(torch.uint8), e.view(torch.uint8)) and not a.requires_grad
+    mobi.mobi_sync_check()

@@ -10,6 +10,10 @@ device, or its handle) the whole call runs as under torch.cuda.stream(stream):
 new outputs belong to that stream too, since memory that the current stream has
 freed may still be in use by work queued there. The inputs are kept alive, and
 ready, by the caller, as for any work queued on another stream.
+
+They serve and have no backward pass: where gradients are recorded, a tensor that
+requires one is refused, since its part of the gradient would be lost in silence.
+Under torch.no_grad() or torch.inference_mode() it is taken as any other.
 """
 from __future__ import annotations
 
@@ -100,8 +104,17 @@ def _call(call: int, device: int, *words) -> None:
         _check(_NAMES[call], status)
 
 
+def _refuse_gradient(what: str) -> None:
+    """For a tensor that requires a gradient."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient and this call has no backward pass: call it under "
+                         "torch.no_grad(), or detach the tensor")
+
+
 def _matrix(t: torch.Tensor, what: str, device: int):
     """(rows, columns, row pitch) of a matrix on CUDA device `device` whose rows are contiguous."""
+    if t.requires_grad:
+        _refuse_gradient(what)
     if t.get_device() != device or device < 0:
         _on(t, what, device)
     if t.dim() != 2:
@@ -127,6 +140,8 @@ def _vector(t, n: int, what: str, device, dtype=None) -> int:
     """The address of a contiguous vector of n elements (None: 0)."""
     if t is None:
         return 0
+    if t.requires_grad:
+        _refuse_gradient(what)
     _on(t, what, device)
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous vector of {n} elements")
@@ -136,6 +151,8 @@ def _vector(t, n: int, what: str, device, dtype=None) -> int:
 
 
 def _scales(s: torch.Tensor, kb: int, rb: int, what: str, device: int) -> int:
+    if s.requires_grad:
+        _refuse_gradient(f"the scale tensor {what}")
     if s.get_device() != device:
         _on(s, f"the scale tensor {what}", device)
     if s.dtype is not torch.float32 or s.shape != (kb, rb) or not s.is_contiguous():
@@ -286,6 +303,8 @@ def mobi_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
             raise ValueError("block must be fp32, bf16 or fp16")
         pwp, pbp = _vector(post_weight, D, "post_weight", d), _vector(post_bias, D, "post_bias", d)
         if gate is not None:
+            if gate.requires_grad:
+                _refuse_gradient("gate")
             _on(gate, "gate", d)
             gdt = _DT.get(gate.dtype, 3)
             if gdt == 3:
