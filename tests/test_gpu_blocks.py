@@ -899,3 +899,91 @@ def test_gradients_are_refused(mobi):
             for a, e in zip(got, want):
                 assert torch.equal(a.view(torch.uint8), e.view(torch.uint8)) and not a.requires_grad
     mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("first", ["quant", "gemm", "gated", "norm", "logprobs"])
+def test_first_call_of_a_process_is_captured(first):
+    """Each call as the first of its process, inside a capture: what it sets up once per device may happen there."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+import block_ref as ref
+import token_adaptive_mixed_b200 as mobi
+first = sys.argv[1]
+g = torch.Generator().manual_seed(2)
+v = torch.randn(40, 256, generator=g).cuda()
+x, xs = ref.operand(40, 256, 1, g)
+w, ws = ref.operand(300, 256, 128, g)
+t = torch.arange(40).cuda()
+call = {"quant": lambda: mobi.mobi_fp8_quant(v), "gemm": lambda: (mobi.mobi_fp8_gemm(x, xs, w, ws),),
+        "gated": lambda: (mobi.mobi_fp8_gated(x, xs, w, ws, w, ws),), "norm": lambda: mobi.mobi_norm(v, block=v),
+        "logprobs": lambda: mobi.mobi_logprobs(v, t, top_k=3)}[first]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = call()
+graph.replay()
+torch.cuda.synchronize()
+mobi.mobi_sync_check()
+for a, b in zip(held, call()):
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+print("same")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "PYTHONPATH": os.pathsep.join([os.path.dirname(here), here])}
+    out = subprocess.run([sys.executable, "-c", code, first], env=env, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
+
+
+def test_outputs_past_32_bits(mobi):
+    """More than 2^31 elements in and out: the last rows are what a call on them alone gives."""
+    g = gen(41)
+    last = torch.tensor([0, 1, 255, 256, -300, -2, -1])
+
+    def pick(t, dim=0):
+        return t.index_select(dim, (last % t.shape[dim]).to(DEV)).contiguous().view(torch.uint8)
+
+    x = torch.randn(1024, 8192, generator=g).to(BF16).to(DEV).repeat(270, 1)[:275001]
+    x[-300:] *= 3
+    part = x[(last % x.shape[0]).to(DEV)]
+    w = (1 + 0.1 * torch.randn(8192, generator=g)).to(BF16).to(DEV)
+    for rows in (1, 128):
+        q, s = mobi.mobi_fp8_quant(x, block_rows=rows)
+        assert q.numel() > 1 << 31
+        if rows == 1:
+            a, b = mobi.mobi_fp8_quant(part)
+            assert torch.equal(pick(q), a.view(torch.uint8)) and torch.equal(pick(s, 1), b.view(torch.uint8))
+        else:
+            at = 128 * (x.shape[0] // 128)
+            a, b = mobi.mobi_fp8_quant(x[at:], block_rows=128)
+            assert torch.equal(q[at:].view(torch.uint8), a.view(torch.uint8)) and torch.equal(s[:, -1:], b)
+        del q, s
+    y = mobi.mobi_norm(x, w)
+    n, en, _, _ = ref.norm(part, w, None, 1e-6, "rms")
+    ref.check_close(y[(last % x.shape[0]).to(DEV)], n, ref.rounded(n, en, BF16))
+    del y, x
+    x = torch.randn(64, 128001, generator=g).to(BF16).to(DEV).repeat(270, 1)
+    t = torch.randint(0, 128001, (x.shape[0],), generator=g).to(DEV)
+    at = (last % x.shape[0]).to(DEV)
+    assert x.numel() > 1 << 31
+    lp, H, top, idx = (o[at] for o in mobi.mobi_logprobs(x, t, top_k=4))
+    wl, wH, wt, wi, elog, eH = ref.logprobs(x[at], t[at], 1.0, 4)
+    assert torch.equal(idx, wi.to(torch.int32))
+    ref.check_close(lp, wl, elog[:, 0] + 6 * ref.U * wl.abs() + 3 * ref.U * elog[:, 0], "log probability")
+    ref.check_close(H, wH, eH, "entropy")
+    ref.check_close(top, wt, elog + 6 * ref.U * wt.abs(), "top")
+    del x
+    T, N, K = 60001, 40003, 144
+    q, s = ref.operand(T, K, 1, g, device=DEV)
+    w, ws = ref.operand(N, K, 128, g, device=DEV)
+    y = mobi.mobi_fp8_gemm(q, s, w, ws, out_dtype=BF16)
+    h, hs = mobi.mobi_fp8_gated(q, s, w, ws, w, ws, out_dtype=E4M3)
+    assert y.numel() > 1 << 31
+    mobi.mobi_sync_check()
+    at = (last % T).to(DEV)
+    qs, ss = q.view(torch.uint8)[at].view(E4M3), s[:, at].contiguous()
+    want, err = ref.product(qs, ss, w, ws)
+    ref.check_close(y[at], want, ref.rounded(want, err, BF16))
+    want, err = ref.gated(qs, ss, w, ws, w, ws, "silu")
+    ref.check_quantised(h.view(torch.uint8)[at].view(E4M3), hs[:, at].contiguous(), want, err)

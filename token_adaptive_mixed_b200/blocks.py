@@ -23,7 +23,8 @@ import struct
 import torch
 
 E4M3 = torch.float8_e4m3fn
-_DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, E4M3: 3}
+_F32 = torch.float32
+_DT = {_F32: 0, torch.bfloat16: 1, torch.float16: 2, E4M3: 3}
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 _NORM = {"none": 0, None: 0, "rms": 1, "layer": 2}
 
@@ -155,7 +156,7 @@ def _scales(s: torch.Tensor, kb: int, rb: int, what: str, device: int) -> int:
         _refuse_gradient(f"the scale tensor {what}")
     if s.get_device() != device:
         _on(s, f"the scale tensor {what}", device)
-    if s.dtype is not torch.float32 or s.shape != (kb, rb) or not s.is_contiguous():
+    if s.dtype is not _F32 or s.shape != (kb, rb) or not s.is_contiguous():
         raise ValueError(f"the scale tensor {what} must be contiguous fp32 of shape ({kb}, {rb})")
     return s.data_ptr()
 
@@ -176,7 +177,7 @@ def _out(t, T: int, N: int, dtype, what, device, dev):
 def _new_scales(t, kb: int, rb: int, what, device, dev):
     """(scales, their address): given ones checked, or new ones."""
     if t is None:
-        t = torch.empty(kb, rb, dtype=torch.float32, device=dev)
+        t = torch.empty(kb, rb, dtype=_F32, device=dev)
         return t, t.data_ptr()
     return t, _scales(t, kb, rb, what, device)
 
@@ -349,10 +350,9 @@ def mobi_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, tem
         raise ValueError("logits must be fp32, bf16 or fp16")
     tp = _vector(targets, T, "targets", d, torch.int64)
     k = int(top_k)
-    f32 = torch.float32
-    lp = None if targets is None else torch.empty(T, dtype=f32, device=dev)
-    en = torch.empty(T, dtype=f32, device=dev) if entropy else None
-    top = torch.empty(T, max(k, 0), dtype=f32, device=dev)
+    lp = None if targets is None else torch.empty(T, dtype=_F32, device=dev)
+    en = torch.empty(T, dtype=_F32, device=dev) if entropy else None
+    top = torch.empty(T, max(k, 0), dtype=_F32, device=dev)
     idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
     _call(_LOGPROBS, d, logits.data_ptr(), dt, T, V, ld, tp, temperature, k, 0 if lp is None else lp.data_ptr(),
           0 if en is None else en.data_ptr(), top.data_ptr(), idx.data_ptr())
