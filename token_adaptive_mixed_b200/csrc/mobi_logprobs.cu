@@ -17,9 +17,11 @@
 // form 128 groups, and the k-th largest of the groups' maxima (k <= 32) is a bound tau
 // that at least k entries reach. Only groups whose maximum reaches it can hold
 // one, so about k/128 of the row is read again, and the entries >= tau are
-// gathered and ranked. (Keeping entries as they come by, against a bound from the first
-// loads, made fp32 rows that L2 cannot hold faster, 272 to 195 us at T = 2048, V = 128000,
-// and bf16 rows slower, 108 to 146 us at V = 128001.) Many equal entries would overflow the gather: then the
+// gathered and ranked. The second reading adds 12%, 43% and 60% to the bytes of fp32 rows
+// for k = 5, 20 and 32, and 8%, 33% and 52% to those of bf16 rows (T = 1024, V = 128000). (Keeping
+// entries as they come by instead, against a bound from the first loads: when fp32 rows took 272 us
+// at T = 2048, V = 128000 that made them 195, and bf16 rows 146 instead of 108 at V = 128001. One form
+// stands for all types, the faster one for 16 bits.) Many equal entries would overflow the gather: then the
 // entries above tau are gathered and the first ones equal to it are found in
 // index order. Where that does not do (even those overflow, or fewer than k
 // groups have an entry above the floor, as under a mask of the type's lowest

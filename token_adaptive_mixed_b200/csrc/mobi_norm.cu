@@ -315,8 +315,10 @@ constexpr int kMaxD = 16384;  // 512 threads x 4 octets
 // with the types of x and the block known to the compiler and values in pairs.
 // Both kernels are bound by issuing (and the barriers between) rather than by memory, so
 // options are tested once a row, not once an octet, and addresses are 32-bit products
-// (T = 8192, D = 4096, x, gate and block bf16, norms on both sides, e4m3 out: general 97 us, this
-// one 55.2 us, of which post costs 12 and the gate 4; without both 39 us at 6.0 TB/s).
+// (T = 8192, D = 4096, x, gate and block bf16, norms on both sides, e4m3 out: this one 55 to 57 us, of
+// which post costs 12 and the gate 4, 39 us at 6.0 TB/s without both; weights and gate fp16 or fp32: 69 and 71.
+// The general kernel takes 117 us there where x alone starts at an odd element, and 190 to 350 us at
+// D = 4095, 4097 and 4100, where every operand's rows are read element by element).
 
 struct Oct {
   float2 v[4];
