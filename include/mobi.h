@@ -621,7 +621,8 @@ MOBI_API mobi_status mobi_fp8_gemm(const void* X, int64_t ldx, const float* xs, 
                                    int64_t ldw, const float* wsc, int64_t N, int out_dtype, void* Y, int64_t ldy,
                                    void* stream);
 
-/* Activations of mobi_fp8_gated: g / (1 + e^-g); g Phi(g); its tanh form; max(g, 0). */
+/* Activations of mobi_fp8_gated: g / (1 + e^-g); g Phi(g); its tanh form; max(g, 0). Computed in fp32 to a few steps of
+ * their value, on the left (where they near 0) to a number of steps that grows with |g|. */
 enum { MOBI_ACT_SILU = 0, MOBI_ACT_GELU = 1, MOBI_ACT_GELU_TANH = 2, MOBI_ACT_RELU = 3 };
 
 /*

@@ -82,8 +82,8 @@ ACT = {
 
 def gated(x, xs, wg, gs, wu, us, act):
     """h = act(g) u and its bound: the slope of every activation is below 1.2. silu's exponential is off by
-    2 + 1.2 |g| steps (its documented bound), its division by 2 more; the forms of gelu add to 1 a function within
-    [-1, 1] that is good to a few steps of 1 (8 with its argument's), which leaves |g| / 2 times that; relu is exact."""
+    2 + 1.2 |g| steps (its documented bound), its division by 2 more; the forms of gelu as 1 plus a function within
+    [-1, 1] that is good to a few steps of 1 (8 with its argument's) leave |g| / 2 times that; relu is exact."""
     g, eg = product(x, xs, wg, gs)
     u, eu = product(x, xs, wu, us)
     a = ACT[act](g)

@@ -987,3 +987,42 @@ def test_outputs_past_32_bits(mobi):
     ref.check_close(y[at], want, ref.rounded(want, err, BF16))
     want, err = ref.gated(qs, ss, w, ws, w, ws, "silu")
     ref.check_quantised(h.view(torch.uint8)[at].view(E4M3), hs[:, at].contiguous(), want, err)
+
+
+@pytest.mark.parametrize("T", [11, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_activations_keep_their_relative_accuracy(mobi, act, T):
+    """g is every finite e4m3 value times a power of two, exactly, and u is 1: h is the activation alone, also far to the
+    left, where it nears 0. Bounds relative to the value (U = 2^-24): the fast exponential of w is off by 2 + 1.2 |w|
+    steps (2 U each), w itself by 6 U |w|, the division by 2 steps, the sum by half of one. gelu with z = |g| / sqrt 2:
+    2 U (7 + z (2 z + 1.5)), from an erfc good to 4 steps whose argument's two roundings, 2 U z, meet a slope of its
+    logarithm of at most 2 z + 1.5, and two products; a polynomial's 14 U and three roundings of z^2 fit into it.
+    Where e^-w passes 2^126 the fast division gives 0, and values below 2^-119 are not held to a relative bound."""
+    codes = torch.arange(256, dtype=torch.uint8).view(E4M3)
+    codes = codes[torch.isfinite(codes.float())]
+    N = codes.numel()
+    x = torch.zeros(T, 128)
+    x[:, 0] = 1.0
+    wg, wu = torch.zeros(N, 128), torch.zeros(N, 128)
+    wg[:, 0], wu[:, 0] = codes.float(), 1.0
+    xs = torch.exp2(-(torch.arange(T) % 11).float())[None].to(DEV)
+    gs, us = torch.ones(1, 2, device=DEV), torch.ones(1, 2, device=DEV)
+    x, wg, wu = (t.to(E4M3).to(DEV) for t in (x, wg, wu))
+    g = codes.double().to(DEV)[None] * xs.double().t()
+    assert torch.equal(mobi.mobi_fp8_gemm(x, xs, wg, gs).double(), g)
+    want = ref.ACT[act](g)
+    if act == "silu":
+        rel = 2 * ref.U * (6 + 1.2 * g.abs())
+    elif act == "gelu_tanh":
+        rel = 2 * ref.U * (6 + 4.2 * (2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)).abs())
+    elif act == "gelu":
+        z = g.abs() / math.sqrt(2.0)
+        rel = 2 * ref.U * (7 + z * (2 * z + 1.5))
+    else:
+        rel = torch.zeros_like(g)
+    # u = 1 for the same xs: the product's other side takes 1 / xs through us, one call for each power of two.
+    for j in range(11):
+        rows = slice(j, T, 11)
+        h = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us * 2.0 ** j, act=act, out_dtype=F32)
+        ref.check_close(h[rows], want[rows], want[rows].abs() * rel[rows] + 2.0 ** -119, f"{act} 2^-{j}")
+    mobi.mobi_sync_check()

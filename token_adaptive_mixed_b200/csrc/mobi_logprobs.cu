@@ -68,12 +68,6 @@ struct Stat {
   float m, s, w;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // a joined with b. A part without entries has m = kLowest, s = w = 0; f > 0 keeps 0 * infinity out of w.
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
   const float m = fmaxf(a.m, b.m);
@@ -89,11 +83,6 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
