@@ -850,9 +850,10 @@ constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 // 23.6 us), by the fewest blocks in a row where one does.
 // From 33 tokens on the kernels' times are estimated from their waves and
 // blocks, in units of 10 ns fitted at K = 4096 and 11008, N = 1024, 4096 and 11008,
-// T = 64 .. 2048; shorter K and narrower N follow from the same terms, unmeasured. Measured at K = 4096, in us, narrow / wide with 128 and with
-// 256 weight rows: T = 64, N = 11008: 15.2 / 23.2 / 22; T = 333, N = 4096: 32 /
-// 14.0 / 20.6; T = 256, N = 11008: - / 24.1 / 22.8; T = 2048, N = 4096: - / 47 / 38.6.
+// T = 64 .. 2048; shorter K and narrower N follow from the same terms, unmeasured.
+// Measured at K = 4096, in us, narrow / wide with 128 and with 256 weight rows: T = 64,
+// N = 11008: 15.2 / 23.2 / 22; T = 333, N = 4096: 32 / 14.0 / 20.6; T = 256, N = 11008:
+// - / 24.1 / 22.8; T = 2048, N = 4096: - / 47 / 38.6.
 static Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   Fp8Plan p;
   const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
