@@ -1026,3 +1026,58 @@ def test_activations_keep_their_relative_accuracy(mobi, act, T):
         h = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us * 2.0 ** j, act=act, out_dtype=F32)
         ref.check_close(h[rows], want[rows], want[rows].abs() * rel[rows] + 2.0 ** -119, f"{act} 2^-{j}")
     mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("T,D", [(1, 256), (7, 256), (700, 512), (7, 257), (1, 1), (5, 8)])
+@pytest.mark.parametrize("xd", [F32, BF16])
+def test_norm_gates_of_any_layout(mobi, T, D, xd):
+    """Whatever broadcasts to the rows: a scalar, one value, a row, a column, transposed, every other column, columns of
+    a larger tensor at odd starts, rows that overlap."""
+    g = gen(T * 3 + D)
+    rnd = lambda *s, dtype=F32: torch.randn(*s, generator=g).to(dtype).to(DEV)  # noqa: E731
+    x, b, w = (rnd(*s, dtype=xd) for s in ((T, D), (T, D), (D,)))
+    for gd in (F32, BF16):
+        r = lambda *s: rnd(*s, dtype=gd)  # noqa: E731
+        gates = [r(1)[0], r(1), r(1, D), r(T, 1), r(1, 1), r(D, T).t(), r(T, 2 * D)[:, ::2], r(T, D + 9)[:, 5:5 + D],
+                 r(T, D + 16)[:, 8:8 + D], r(2 * T, D)[::2], r(T + D).as_strided((T, D), (1, 1)), r(T, 3)[:, 1:2],
+                 r(D, 1).t().expand(T, D), r(D, 3)[:, 1]]
+        for i, gate in enumerate(gates):
+            check_norm(mobi, dict(x=x, weight=w, bias=None, eps=1e-6, kind="rms", block=b, gate=gate, scale=-1.5),
+                       (F32, E4M3)[i % 2])
+
+
+@pytest.mark.parametrize("T,K", [(1, 128), (7, 300), (130, 513), (260, 1024)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_quant_and_norm_into_given_outputs(mobi, T, K, dtype):
+    """Codes and scales written where the caller says, at rows on multiples of 16 bytes and off them, and nowhere else."""
+    g = gen(T + K)
+    x = torch.randn(T, K, generator=g).to(dtype)
+    d = x.to(DEV)
+    kb = (K + 127) // 128
+    n, en, _, _ = ref.norm(d, None, None, 1e-6, "rms")
+    for off in (0, 16, 3):
+        for rows in (1, 128):
+            q, check = guarded(T, K, E4M3, off)
+            room = torch.full((kb * (T if rows == 1 else (T + 127) // 128) + 2,), 7.0, device=DEV)
+            s = room[1:-1].view(kb, -1)
+            a, b = mobi.mobi_fp8_quant(d, block_rows=rows, Q=q, scale=s)
+            assert a is q and b is s
+            wq, ws = ref.quant(x, rows)
+            assert same_codes(q, wq) and torch.equal(s.cpu(), ws) and (room[[0, -1]] == 7.0).all()
+            check()
+        q, check = guarded(T, K, E4M3, off)
+        room = torch.full((kb * T + 2,), 7.0, device=DEV)
+        s = room[1:-1].view(kb, T)
+        a, b = mobi.mobi_norm(d, out_dtype=E4M3, N=q, n_scale=s)
+        assert a is q and b is s
+        ref.check_quantised(q, s, n, en)
+        assert (room[[0, -1]] == 7.0).all()
+        check()
+        y, check = guarded(T, K, dtype, off)
+        r, checked = guarded(T, K, dtype, 16 - off)
+        o, rr = mobi.mobi_norm(d, block=d, scale=0.0, out_dtype=dtype, N=y, R=r)
+        assert o is y and rr is r and torch.equal(r, d)
+        ref.check_close(y, n, ref.rounded(n, en, dtype))
+        check()
+        checked()
+    mobi.mobi_sync_check()
