@@ -1081,3 +1081,31 @@ def test_quant_and_norm_into_given_outputs(mobi, T, K, dtype):
         check()
         checked()
     mobi.mobi_sync_check()
+
+
+@pytest.mark.parametrize("T", [11, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_activations_of_infinities_and_nan(mobi, act, T):
+    """g beyond fp32's range (the scales' product overflows) and NaN, u = 1: what the formula gives in 64 bits, in those
+    rows alone."""
+    N = 260
+    g = gen(T)
+    x = torch.zeros(T, 128)
+    x[:, 0] = 1.0
+    wg, wu = torch.zeros(N, 128), torch.zeros(N, 128)
+    wg[:, 0], wu[:, 0] = torch.randn(N, generator=g), 1.0
+    wg[7, 0] = 0.0
+    xs = torch.ones(1, T)
+    xs[0, 3], xs[0, 5] = 2.0 ** 127, float("nan")
+    gs, us = torch.full((1, 3), 4.0, device=DEV), torch.full((1, 3), 2.0 ** -127, device=DEV)
+    x, wg, wu = (t.to(E4M3).to(DEV) for t in (x, wg, wu))
+    xs = xs.to(DEV)
+    v = wg.double()[:, 0]
+    big = torch.where(v == 0, math.nan, v.sign() * math.inf)  # 0 times an infinite scale
+    h = mobi.mobi_fp8_gated(x, xs, wg, gs, wu, us, act=act, out_dtype=F32)
+    for row, want in ((3, ref.ACT[act](big)), (5, torch.full_like(v, math.nan))):
+        assert torch.equal(torch.isnan(h[row]), torch.isnan(want))
+        assert torch.equal(h[row][~torch.isnan(want)].double(), want[~torch.isnan(want)])
+    rest = [t for t in range(T) if t not in (3, 5)]
+    assert torch.isfinite(h[rest]).all()
+    mobi.mobi_sync_check()

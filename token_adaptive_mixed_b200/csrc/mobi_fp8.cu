@@ -58,12 +58,14 @@ __device__ __forceinline__ float normal_tail(float a) {
 // 2 sqrt(2 / pi) (g + 0.044715 g^3), use the fast exponential and division, off by a few fp32
 // steps and by about 1.2 |w| more where e^-w counts. gelu is max(g, 0) - |g| Phi(-|g|), off by a few steps and,
 // on the left, by the argument's rounding times g^2. (T = 2048, N = 11008, K = 4096, gelu: 1 + erf, which loses
-// its value there, 197 us; erfc 220; this 193. The tanh form by tanh 194, by the exponential 189.)
+// its value there, 197 us; erfc 220; this 197. The tanh form by tanh 194, by the exponential 189.)
 template <int ACT>
 __device__ __forceinline__ float activate_as(float g) {
   if (ACT == kSilu) return __fdividef(g, 1.0f + __expf(-g));
   if (ACT == kGelu) {
-    const float a = fminf(fabsf(g), 64.0f);  // the tail is 0 from 15 on; an infinite a times 0 would be NaN
+    // |g|, cut at 64 on the right, where the tail is 0 from 15 on: an infinite g stays infinite there and becomes NaN
+    // on the left, as in the formula.
+    const float a = fmaxf(-g, fminf(g, 64.0f));
     return fmaf(-a, normal_tail(a), max_nan(g, 0.0f));
   }
   if (ACT == kGeluTanh) return __fdividef(g, 1.0f + __expf(-1.59576912160573071f * fmaf(0.044715f * g * g, g, g)));
